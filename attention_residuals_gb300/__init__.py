@@ -3,6 +3,14 @@
 The hot path lives in libattnres_gb300.so (C ABI: include/attnres.h); this
 package is its thin Python binding plus seeded workload generators.
 """
+from .cached import (  # noqa: F401
+    attnres_cache_load,
+    attnres_cache_row_bytes,
+    attnres_cache_write,
+    attnres_cached,
+    attnres_cached_bwd,
+    attnres_cached_fwd,
+)
 from .ops import (  # noqa: F401
     EPS_DEFAULT,
     attnres,

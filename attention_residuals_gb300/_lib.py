@@ -45,6 +45,12 @@ EXPORTED = [
     "attnres_selected_bwd_workspace_bytes",
     "attnres_fwd_partial",
     "attnres_bwd_partial",
+    "attnres_cache_row_bytes",
+    "attnres_cache_write",
+    "attnres_cache_load",
+    "attnres_cached_fwd",
+    "attnres_cached_bwd",
+    "attnres_cached_bwd_workspace_bytes",
     "attnres_step_host",
     "attnres_step_host_workspace_bytes",
     "attnres_fwd_withhold_for_test",
@@ -73,6 +79,24 @@ class AttnresMultiParams(ctypes.Structure):
         ("M", ctypes.c_int32),
         ("out_ld_m", ctypes.c_int64),
         ("out_ld_n", ctypes.c_int64),
+    ]
+
+
+class AttnresCachedParams(ctypes.Structure):
+    _fields_ = [
+        ("S", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("R", ctypes.c_int32),
+        ("key_offset", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("out_norm", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("row_ld", ctypes.c_int64),
+        ("live_ld", ctypes.c_int64),
+        ("live", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p * MAX_S),
     ]
 
 
@@ -189,6 +213,20 @@ def load(path: str | None = None):
         lib.attnres_selected_bwd.restype = ctypes.c_int
         lib.attnres_selected_bwd.argtypes = [MP, vp, i32, vp, vp, fp, fp, fp, ctypes.POINTER(ctypes.c_void_p),
                                              i64, vp, fp, vp, sz, vp]
+        lib.attnres_cache_row_bytes.restype = sz
+        lib.attnres_cache_row_bytes.argtypes = [i32, i32]
+        lib.attnres_cache_write.restype = ctypes.c_int
+        lib.attnres_cache_write.argtypes = [vp, i64, i64, i32, i32, i32, i32, vp, i64, vp]
+        lib.attnres_cache_load.restype = ctypes.c_int
+        lib.attnres_cache_load.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
+        CP = ctypes.POINTER(AttnresCachedParams)
+        lib.attnres_cached_fwd.restype = ctypes.c_int
+        lib.attnres_cached_fwd.argtypes = [CP, vp, vp, vp, fp, fp, fp, fp, vp]
+        lib.attnres_cached_bwd_workspace_bytes.restype = sz
+        lib.attnres_cached_bwd_workspace_bytes.argtypes = [CP]
+        lib.attnres_cached_bwd.restype = ctypes.c_int
+        lib.attnres_cached_bwd.argtypes = [CP, vp, vp, vp, fp, fp, fp, fp, ctypes.POINTER(ctypes.c_void_p), i64, vp,
+                                           i64, vp, fp, vp, fp, vp, sz, vp]
         _lib = lib
         return lib
 

@@ -33,6 +33,7 @@ enum WaitSite : unsigned {
     kSiteBadId = 7,  // a selected-query id outside [0, E)
     kSiteBwdExchange = 8,  // a cluster peer's partial sums did not arrive
     kSiteBounds = 9,       // debug build: a store's indices fell outside the call's sizes
+    kSiteCacheTag = 10,    // a cache record's tag is not the call's
 };
 
 // Debug build (-DATTNRES_DEBUG, a stand-in for a memory checker): a global

@@ -26,6 +26,7 @@ import torch
 from torch import Tensor
 
 from . import _lib
+from . import cached as _cached
 from . import ops as _ops
 
 _NS = "attnres_gb300"
@@ -398,3 +399,151 @@ def attnres_block_read_op(completed, partial: Tensor, delta: Tensor, query: Tens
     ko = D - query.numel() if key_offset is None else int(key_offset)
     out = read_block_fwd(comp + [partial], delta, query, out_norm_weight, float(eps), float(scale), ko)
     return out[0], out[1]
+
+
+# --------------------------------------------------------------------------
+# Compressed source cache
+# --------------------------------------------------------------------------
+def _cache_bytes(D: int, bits: int) -> int:
+    # the C library's attnres_cache_row_bytes, for symbolic shapes' sake in plain arithmetic
+    codes = (D * bits // 8 + 15) // 16 * 16
+    return (codes + ((D + 31) // 32 + 7) // 8 * 8 + 8 + 15) // 16 * 16
+
+
+@torch.library.custom_op(f"{_NS}::cache_write", mutates_args=(), device_types="cuda")
+def cache_write(values: Tensor, bits: int, key_rank: int, key_offset: int) -> Tensor:
+    return _cached.attnres_cache_write(values, bits=bits, key_rank=key_rank, key_offset=key_offset)
+
+
+@cache_write.register_fake
+def _(values, bits, key_rank, key_offset):
+    return torch.empty((*values.shape[:-1], _cache_bytes(values.shape[-1], bits)), dtype=torch.uint8,
+                       device=values.device)
+
+
+@torch.library.custom_op(f"{_NS}::cache_load", mutates_args=(), device_types="cuda")
+def cache_load(rows: Tensor, D: int, bits: int) -> Tensor:
+    return _cached.attnres_cache_load(rows, D, bits=bits)
+
+
+@cache_load.register_fake
+def _(rows, D, bits):
+    return torch.empty((*rows.shape[:-1], D), dtype=torch.bfloat16, device=rows.device)
+
+
+def _records(rows: List[Tensor], packed: bool):
+    return rows[0] if packed else list(rows)
+
+
+def _record_shape(rows: List[Tensor], packed: bool):
+    """(sources, leading shape, tokens)"""
+    lead = tuple(rows[0].shape[1:-1]) if packed else tuple(rows[0].shape[:-1])
+    N = 1
+    for d in lead:
+        N *= d
+    return (rows[0].shape[0] if packed else len(rows)), lead, N
+
+
+@torch.library.custom_op(f"{_NS}::read_cached_fwd", mutates_args=(), device_types="cuda")
+def read_cached_fwd(rows: List[Tensor], values: List[Tensor], live: Optional[Tensor], q: Tensor,
+                    w_o: Optional[Tensor], D: int, bits: int, eps: float, scale: float, key_offset: int,
+                    packed: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    S, lead, N = _record_shape(rows, packed)
+    S += live is not None
+    # a registered operator's outputs may not share memory: statistics of their own
+    out = {k: torch.empty((N, S), dtype=torch.float32, device=q.device) for k in ("alpha", "rstd", "logit")}
+    r = _cached.attnres_cached_fwd(_records(rows, packed), q, D, bits=bits, live=live, w_o=w_o, eps=eps, scale=scale,
+                                   key_offset=key_offset, out=out)
+    o_rstd = r["o_rstd"] if r["o_rstd"] is not None else torch.empty((0,), dtype=torch.float32, device=q.device)
+    return r["y"], r["alpha"], r["rstd"], r["logit"], o_rstd
+
+
+@read_cached_fwd.register_fake
+def _(rows, values, live, q, w_o, D, bits, eps, scale, key_offset, packed):
+    S, lead, N = _record_shape(rows, packed)
+    S += live is not None
+    f32 = dict(dtype=torch.float32, device=q.device)
+    y = torch.empty((*lead, D), dtype=torch.bfloat16, device=q.device)
+    stats = [torch.empty((N, S), **f32) for _ in range(3)]
+    return y, *stats, torch.empty((N if w_o is not None else 0,), **f32)
+
+
+@torch.library.custom_op(f"{_NS}::read_cached_bwd", mutates_args=(), device_types="cuda")
+def read_cached_bwd(rows: List[Tensor], live: Optional[Tensor], q: Tensor, w_o: Optional[Tensor], dy: Tensor,
+                    alpha: Tensor, rstd: Tensor, logit: Tensor, o_rstd: Tensor, D: int, bits: int, eps: float,
+                    scale: float, key_offset: int, packed: bool, need_dvalues: bool,
+                    packed_values: bool) -> Tuple[List[Tensor], Tensor, Tensor, Tensor, Tensor, Tensor]:
+    saved = {"alpha": alpha, "rstd": rstd, "logit": logit, "o_rstd": o_rstd if o_rstd.numel() else None}
+    S, lead, N = _record_shape(rows, packed)
+    dv = None
+    if need_dvalues:
+        dv = torch.empty((S, *lead, D), dtype=torch.bfloat16, device=q.device) if packed_values else \
+            [torch.empty((*lead, D), dtype=torch.bfloat16, device=q.device) for _ in range(S)]
+    g = _cached.attnres_cached_bwd(_records(rows, packed), q, dy.contiguous(), saved, D, bits=bits, live=live, w_o=w_o,
+                                   eps=eps, scale=scale, key_offset=key_offset, need_dvalues=need_dvalues, dvalues=dv)
+    none16 = torch.empty((0,), dtype=torch.bfloat16, device=q.device)
+    none32 = torch.empty((0,), dtype=torch.float32, device=q.device)
+    has_w = w_o is not None
+    return ([dv] if need_dvalues and packed_values else list(dv or []),
+            g["d_live"] if live is not None else none16, g["dq"].view_as(q),
+            g["dw_o"] if has_w else none16.clone(), g["dq_f32"].view(q.shape),
+            g["dw_o_f32"] if has_w else none32)
+
+
+@read_cached_bwd.register_fake
+def _(rows, live, q, w_o, dy, alpha, rstd, logit, o_rstd, D, bits, eps, scale, key_offset, packed, need_dvalues,
+      packed_values):
+    S, lead, N = _record_shape(rows, packed)
+    b16, f32 = dict(dtype=torch.bfloat16, device=q.device), dict(dtype=torch.float32, device=q.device)
+    dv = [] if not need_dvalues else [torch.empty((S, *lead, D), **b16)] if packed_values else \
+        [torch.empty((*lead, D), **b16) for _ in range(S)]
+    dl = torch.empty((*lead, D), **b16) if live is not None else torch.empty((0,), **b16)
+    nw = D if w_o is not None else 0
+    return dv, dl, torch.empty_like(q), torch.empty((nw,), **b16), torch.empty(q.shape, **f32), torch.empty((nw,), **f32)
+
+
+def _cached_setup_context(ctx, inputs, output):
+    rows, values, live, q, w_o, D, bits, eps, scale, key_offset, packed = inputs
+    y, alpha, rstd, logit, o_rstd = output
+    ctx.cfg = (D, bits, eps, scale, key_offset, packed)
+    ctx.nvalues = len(values)
+    ctx.packed_values = len(values) > 0 and values[0].dim() == rows[0].dim() + (0 if packed else 1)
+    ctx.has_live, ctx.has_w = live is not None, w_o is not None
+    none = q.new_empty((0,))
+    ctx.save_for_backward(q, w_o if ctx.has_w else none, live if ctx.has_live else none, alpha, rstd, logit, o_rstd,
+                          *rows)
+
+
+def _cached_backward(ctx, dy, d_alpha, d_rstd, d_logit, d_orstd):
+    q, w_o, live, alpha, rstd, logit, o_rstd, *rows = ctx.saved_tensors
+    D, bits, eps, scale, key_offset, packed = ctx.cfg
+    dv, dlive, dq, dw, _, _ = read_cached_bwd(
+        list(rows), live if ctx.has_live else None, q, w_o if ctx.has_w else None, dy.to(torch.bfloat16), alpha, rstd,
+        logit, o_rstd, D, bits, eps, scale, key_offset, packed, ctx.nvalues > 0, ctx.packed_values)
+    return ([None] * len(rows), list(dv), dlive if ctx.has_live else None, dq, dw.view_as(w_o) if ctx.has_w else None,
+            None, None, None, None, None, None)
+
+
+read_cached_fwd.register_autograd(_cached_backward, setup_context=_cached_setup_context)
+
+
+def attnres_cached_op(rows, query: Tensor, D: int, *, bits: int = 8, values=None, live: Optional[Tensor] = None,
+                      eps: float = _ops.EPS_DEFAULT, scale: float = 1.0, out_norm_weight: Optional[Tensor] = None,
+                      key_offset: Optional[int] = None) -> Tensor:
+    """The read over cached sources through the registered operator."""
+    recs, packed = _pack_args(rows)
+    if not recs:
+        raise ValueError("need at least one cached source")
+    vals = [] if values is None else _pack_args(values)[0]
+    if vals:
+        S, lead, _ = _record_shape(recs, packed)
+        one = isinstance(values, Tensor)
+        if len(vals) != (1 if one else S) or any(tuple(v.shape) != ((S, *lead, D) if one else (*lead, D)) for v in vals):
+            raise ValueError("values must be the tensors the records were written from, one per cached source")
+        if any(v.dtype != torch.bfloat16 for v in vals):
+            raise TypeError("values must be torch.bfloat16")
+        if not any(v.requires_grad for v in vals):
+            vals = []
+    ko = D - query.numel() if key_offset is None else int(key_offset)
+    return read_cached_fwd(recs, vals, live, query, out_norm_weight, int(D), int(bits), float(eps), float(scale), ko,
+                           packed)[0]

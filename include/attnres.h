@@ -293,7 +293,8 @@ attnres_status attnres_step_host(const attnres_params* p, const void* q, const v
  * store of an output whose indices fall outside the call's sizes (skipped,
  * never made).  This call synchronises the device, returns
  * ATTNRES_ERR_DEVICE and clears the record if one was set, ATTNRES_OK
- * otherwise.
+ * otherwise.  A record of the compressed cache whose tag is not the call's
+ * is recorded here too.
  */
 attnres_status attnres_check_device_error(void);
 
@@ -455,6 +456,109 @@ attnres_status attnres_selected_bwd(const attnres_multi_params* p, const void* b
                                     const float* rstd, const float* logit, void* const* dsrc,
                                     int64_t dsrc_ld, void* dbank, float* dbank_f32, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Compressed source cache.  Every source of an AttnRes stack is written once
+ * and read by all later layers; the cache holds its rows in 8 or 4 bits per
+ * channel, and the read works on them directly.  One record per token:
+ *
+ *   codes    bits 8: D e4m3 bytes; bits 4: D e2m1 nibbles, channel 2i in the
+ *            low half of byte i; zeros up to a multiple of 16 bytes
+ *   scales   one byte per 32 channels: k + 127, the group's scale being 2^k
+ *   stat     float, at the next multiple of 8 bytes: mean square of the key
+ *            channels' values, as the codes stand for them
+ *   tag      uint32: R | key_offset << 14 | (bits == 8) << 27 | 5 << 28
+ *   zeros up to a multiple of 16 bytes
+ *
+ * k is the smallest exponent, at least -110, for which the group's largest
+ * magnitude is at most 448 * 2^k (bits 8) or 6 * 2^k (bits 4); a code is the
+ * value times 2^-k rounded to nearest, ties to even.  A value read back is
+ * code * 2^k, exact in bf16.  Magnitudes above 1.5 * 2^127 are held as that;
+ * a group with a NaN or an infinity reads back as NaN, all of it.
+ *
+ * Records hold the key slice they were written for (R, key_offset).  A read
+ * for another one, or of records that no write filled, is recorded for
+ * attnres_check_device_error and that source's statistics, with the token's
+ * output, are NaN.  Loading a record of another format gives NaN likewise.
+ * Conventions as at the top; records start on 16-byte boundaries.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one record (a multiple of 16); 0 for a D or bits the cache does not take. */
+size_t attnres_cache_row_bytes(int32_t D, int32_t bits);
+
+/*
+ * Quantise N bf16 rows (src + n * src_ld elements) into records
+ * (rows + n * row_ld bytes; row_ld >= attnres_cache_row_bytes, % 16 == 0;
+ * must not overlap src).  Every byte of a record is written, nothing between
+ * records is.  A part of a source is written by pointing at its first token.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA.
+ */
+attnres_status attnres_cache_write(const void* src, int64_t src_ld, int64_t N, int32_t D, int32_t bits, int32_t R,
+                                   int32_t key_offset, void* rows, int64_t row_ld, void* stream);
+
+/* Read N records back as bf16 rows (dst + n * dst_ld elements).  Errors as
+ * attnres_cache_write. */
+attnres_status attnres_cache_load(const void* rows, int64_t row_ld, int64_t N, int32_t D, int32_t bits, void* dst,
+                                  int64_t dst_ld, void* stream);
+
+/*
+ * A read over cached sources.
+ *   S            cached sources, 1 <= S; with the live one at most ATTNRES_MAX_S
+ *   D, R, key_offset, N, eps, scale, out_norm   as for attnres_params
+ *   bits         8 or 4, the records' format
+ *   row_ld       bytes between consecutive tokens' records of a source
+ *   rows[s]      device pointer to source s's records; the same pointer may
+ *                appear more than once
+ *   live         NULL, or one more source in bf16 that is not cached (such as
+ *                the current partial block sum), read last: source S of the
+ *                statistics; row n at live + n * live_ld elements
+ */
+typedef struct {
+    int32_t S;
+    int32_t D;
+    int32_t R;
+    int32_t key_offset;
+    int64_t N;
+    float eps;
+    float scale;
+    int32_t out_norm;
+    int32_t bits;
+    int64_t row_ld;
+    int64_t live_ld;
+    const void* live;
+    const void* rows[ATTNRES_MAX_S];
+} attnres_cached_params;
+
+/*
+ * The read of attnres_fwd with the records' values as sources.  Outputs:
+ * y bf16 [N, D]; alpha, rstd, logit f32 [N, S (+ 1 with live)]; o_rstd f32
+ * [N], required iff out_norm.  w_o starts on a 16-byte boundary.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA.
+ */
+attnres_status attnres_cached_fwd(const attnres_cached_params* p, const void* q, const void* w_o, void* y, float* alpha,
+                                  float* rstd, float* logit, float* o_rstd, void* stream);
+
+/* Bytes of workspace attnres_cached_bwd needs (0 when N == 0): FP32 partial
+ * rows of dq and dw_o. */
+size_t attnres_cached_bwd_workspace_bytes(const attnres_cached_params* p);
+
+/*
+ * Gradient of attnres_cached_fwd: as attnres_bwd, with the records' values as
+ * the sources, and the forward's alpha, rstd, logit and o_rstd.
+ *   dsrc    host array of S device pointers (gradient of the values that
+ *           source s's codes stand for: the straight-through gradient of what
+ *           was written; bf16 rows dsrc_ld elements apart), or NULL when the
+ *           cached sources need none
+ *   dlive   gradient of the live source, or NULL when it needs none
+ *   dq, dq_f32, dw_o, dw_o_f32, workspace   as for attnres_bwd
+ * Gradient rows must not overlap each other, the records, live or dy.
+ * dq and dw_o are bitwise reproducible.  Errors: as above, plus WORKSPACE.
+ */
+attnres_status attnres_cached_bwd(const attnres_cached_params* p, const void* q, const void* w_o, const void* dy,
+                                  const float* alpha, const float* rstd, const float* logit, const float* o_rstd,
+                                  void* const* dsrc, int64_t dsrc_ld, void* dlive, int64_t dlive_ld, void* dq,
+                                  float* dq_f32, void* dw_o, float* dw_o_f32, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 #ifdef __cplusplus
 }
