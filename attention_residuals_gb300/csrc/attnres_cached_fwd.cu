@@ -17,8 +17,6 @@ namespace {
 
 __device__ unsigned g_cached_fwd_error;
 
-constexpr int RB = 4;  // rows per block
-
 // The query's 32 channels of this thread as halves, scaled by a power of two
 // that puts the largest magnitude in [2^14, 2^15) (`back` undoes it).  bf16
 // has fewer significand bits than a half, so every channel down to 2^-28 of
@@ -49,201 +47,374 @@ __device__ __forceinline__ void load_query(const CachedArgs& a, int c0, uint32_t
     any = c0 < a.ko + a.R && c0 + 32 > a.ko;
 }
 
-// Sums over the team: LW lanes of a warp, and all `warps` of the CTA when a
-// team is more than one warp.  `red` is one of two buffers used in turn, so
-// one barrier per call is enough.
-template <int K, int LW, bool MULTI>
-__device__ __forceinline__ void team_sum(float (&v)[K], float* red, int warps) {
-#pragma unroll
-    for (int o = LW / 2; o > 0; o >>= 1) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+// Shared memory of one warp: kStages segments of raw rows, then the
+// segment's coefficients.  A row of a segment is the codes of the warp's 32
+// threads (16 or 32 bytes each), then the scales and the statistics of its
+// tokens.  A warp fills and reads its own part only, so the copies need no
+// barrier wider than the warp.
+constexpr int kStages = 2;
+constexpr int kSegmentBytes = 5632;  // of a warp's rows in one stage (20 warps of an SM, two stages: 220 KB)
+
+template <int BITS, int LW>
+struct Seg {
+    static constexpr int CH = BITS / 4;                           // 16-byte chunks of codes a thread
+    static constexpr int TW = 32 / LW;                            // tokens a warp
+    static constexpr int SC = LW >= 8 ? 32 : TW * 8;              // scale bytes a row
+    static constexpr int ROW = 512 * CH + SC + 8 * TW;            // bytes a row
+    static constexpr int MOST = kSegmentBytes / ROW;
+    __host__ __device__ static int rows(int S) {                  // rows a segment
+        const int n = (S + MOST - 1) / MOST;
+        return (S + n - 1) / n;
     }
-    if constexpr (MULTI) {
-        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-        if (lane == 0) {
+    __host__ __device__ static int stage(int seg) { return (seg * ROW + 15) & ~15; }
+    __host__ __device__ static int coef(int seg) { return (TW * (seg + 2) * 4 + 15) & ~15; }
+    __host__ __device__ static int warp(int seg) { return kStages * stage(seg) + 2 * coef(seg); }
+};
+
+// 16-byte asynchronous copy past L1; zeros where !on (the source is not read).
+__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int LW>
+__device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) red[w * K + i] = v[i];
+    for (int o = LW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+template <int LW>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+    for (int o = LW / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// Sums of four values over the LW lanes of a team; afterwards the team's lane
+// 0 writes them to out[0..3] (only the first `rows`).
+template <int LW>
+__device__ __forceinline__ void lanes_sum4(float (&p)[4], float* out, int rows) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (LW == 32) {  // one lane in eight ends up with one of the sums
+        warp_reduce_scatter<4>(p, lane);
+        if ((lane & 7) == 0 && (lane >> 3) < rows) out[lane >> 3] = p[0];
+    } else {
+#pragma unroll
+        for (int o = LW / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] += __shfl_xor_sync(0xffffffffu, p[i], o);
         }
-        __syncthreads();
+        if (lane % LW == 0) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) v[i] = 0.0f;
-        for (int u = 0; u < warps; ++u) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) v[i] += red[u * K + i];
+            for (int i = 0; i < 4; ++i)
+                if (i < rows) out[i] = p[i];
         }
     }
 }
 
-template <int BITS, int LW, bool MULTI, bool NORM>
-__global__ void __launch_bounds__(256) cached_fwd_kernel(const CachedArgs a) {
-    __shared__ float red[2][8 * RB];
-    extern __shared__ float zbuf_all[];  // [teams][2 * sources]: logits, reciprocal RMS
+template <int BITS, int LW, bool MULTI, bool NORM, bool LIVE>
+__global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) {
+    using G = Seg<BITS, LW>;
+    constexpr int CH = G::CH, TW = G::TW;
+    extern __shared__ __align__(16) unsigned char dyn[];
     pdl_wait();
-    const int warps = blockDim.x >> 5;
-    const int T = MULTI ? blockDim.x : LW;
-    const int teams = MULTI ? 1 : blockDim.x / LW;
-    const int team = MULTI ? 0 : threadIdx.x / LW, t = MULTI ? threadIdx.x : threadIdx.x % LW;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int l = lane % LW, tw = lane / LW;                   // lane of the team, team of the warp
+    const int t = MULTI ? threadIdx.x : l;                     // thread of the team
     const int c0 = t * 32;
-    const int SL = a.S + (a.live ? 1 : 0);
-    float* zbuf = zbuf_all + team * 2 * SL;
+    const int SL = a.S + (LIVE ? 1 : 0);
+    const int seg = G::rows(a.S), nseg = (a.S + seg - 1) / seg;
+    const int groups = (a.D + 31) / 32;
+    unsigned char* mine = dyn + wid * G::warp(seg);
+    float* coef = reinterpret_cast<float*>(mine + kStages * G::stage(seg)) + tw * (seg + 2);
+    // dots of a segment: per warp, or for all warps of a team in two buffers used in turn
+    unsigned char* rest = dyn + warps * G::warp(seg);
+    float* red = MULTI ? reinterpret_cast<float*>(rest)
+                       : reinterpret_cast<float*>(mine + kStages * G::stage(seg) + G::coef(seg)) + tw * (seg + 2);
+    if (MULTI) rest += (2 * warps * (seg + 2) * 4 + 15) & ~15;
+    float* zbuf = reinterpret_cast<float*>(rest) + (MULTI ? 0 : (wid * TW + tw) * 2 * SL);  // logits, then 1 / RMS
+    const unsigned char** rows = reinterpret_cast<const unsigned char**>(
+        rest + ((static_cast<size_t>(MULTI ? 1 : warps * TW) * 2 * SL * 4 + 15) & ~size_t(15)));
+    for (int s = threadIdx.x; s < a.S; s += blockDim.x) rows[s] = a.rows[s];
     uint32_t q[16];
     float back;
     bool key;
     load_query(a, c0, q, back, key);
     const bool has = c0 < a.D;
-    int flip = 0;
-    const long long stride = static_cast<long long>(gridDim.x) * teams;
-    for (long long base = static_cast<long long>(blockIdx.x) * teams; base < a.N; base += stride) {
-        const bool valid = base + team < a.N;
-        const long long n = valid ? base + team : a.N - 1;
+    const bool warp_key = __any_sync(0xffffffffu, key);
+    __syncthreads();
+
+    // tokens of a CTA step: one for a team of several warps, else TW a warp
+    const int per = MULTI ? 1 : warps * TW;
+    const long long stride = static_cast<long long>(gridDim.x) * per;
+    const long long first = static_cast<long long>(blockIdx.x) * per + (MULTI ? 0 : wid * TW);
+    if (first >= a.N) return;  // whole warps only (a team of several warps shares `first`)
+
+    const uint32_t st0 = smem_u32(mine);
+    auto issue = [&](int stage, long long n0, int g) {
+        const uint32_t base = st0 + stage * G::stage(seg);
+        const int s0 = g * seg, cnt = min(seg, a.S - s0);
+        long long off[CH];
+        bool on[CH];
+        uint32_t dst[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = lane + 32 * i;
+            const int team = c / (LW * CH), x = (c % (LW * CH) + (MULTI ? wid * 32 * CH : 0)) * 16;
+            off[i] = min(n0 + team, a.N - 1) * a.row_ld + x;
+            on[i] = x < static_cast<int>(a.codes);
+            if (!on[i]) off[i] -= x;
+            dst[i] = base + (CH == 2 ? c ^ ((c >> 3) & 1) : c) * 16;  // keeps the 32-byte reads off each other's banks
+        }
+        for (int r = 0; r < cnt; ++r) {
+            const unsigned char* p = rows[s0 + r];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) cp_async_16z(dst[i] + r * 512 * CH, p + off[i], on[i]);
+        }
+        const uint32_t sc = base + seg * 512 * CH, stt = sc + seg * G::SC;
+        if constexpr (LW >= 16) {
+            constexpr int H = LW / 16;  // chunks of 16 scales a token
+            for (int i = lane; i < cnt * TW * H; i += 32) {
+                const int r = i / (TW * H), team = i / H % TW, h = i % H;
+                const int x = (MULTI ? wid * 32 : 0) + h * 16;
+                if (x < groups)
+                    cp_async_16z(sc + r * 32 + team * LW + h * 16,
+                                 rows[s0 + r] + min(n0 + team, a.N - 1) * a.row_ld + a.codes + x, true);
+            }
+        } else {
+            for (int i = lane; i < cnt * TW; i += 32) {
+                const int r = i / TW, team = i % TW;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sc + r * G::SC + team * 8),
+                             "l"(rows[s0 + r] + min(n0 + team, a.N - 1) * a.row_ld + a.codes)
+                             : "memory");
+            }
+        }
+        for (int i = lane; i < cnt * TW; i += 32) {
+            const int r = i / TW, team = i % TW;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(stt + i * 8),
+                         "l"(rows[s0 + r] + min(n0 + team, a.N - 1) * a.row_ld + a.stat)
+                         : "memory");
+        }
+        cp_async_commit();
+    };
+    auto codes = [&](uint32_t base, int r, uint32_t (&h)[16]) {
+        CacheCodes<BITS> w;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = lane * CH + i;
+            const uint4 u = lds128(base + r * 512 * CH + (CH == 2 ? c ^ ((c >> 3) & 1) : c) * 16);
+            w.w[4 * i] = u.x, w.w[4 * i + 1] = u.y, w.w[4 * i + 2] = u.z, w.w[4 * i + 3] = u.w;
+        }
+        w.unpack(h);
+    };
+    auto scale_of = [&](uint32_t base, int r) {
+        uint32_t b;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(base + seg * 512 * CH + r * G::SC + (LW >= 8 ? lane : tw * 8 + l)));
+        return has ? cache_scale(b) : 0.0f;
+    };
+
+    issue(0, first, 0);
+    int stage = 0, flip = 0;
+    for (long long n0 = first; n0 < a.N; n0 += stride) {
+        const bool valid = n0 + tw < a.N;
+        const long long n = valid ? n0 + tw : a.N - 1;
+        uint4 lv[4];
+        if constexpr (LIVE) {
+            const uint16_t* x = a.live + n * a.live_ld + c0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lv[i] = c0 + 8 * i < a.D ? ld_global_nc_v4(x + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        }
         float2 acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.0f, 0.0f);
         float mx = __uint_as_float(0xff800000u), sum = 0.0f;
-        for (int s0 = 0; s0 < a.S; s0 += RB) {
-            uint32_t h[RB][16];
-            float sc[RB], p[RB], rs[RB];
+        for (int g = 0; g < nseg; ++g) {
+            // the next segment (of this token or the next one) is copied while this one is read
+            const bool last = g == nseg - 1;
+            if (!last || n0 + stride < a.N) {
+                issue(stage ^ 1, last ? n0 + stride : n0, last ? 0 : g + 1);
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
+            __syncwarp();
+            const uint32_t base = st0 + stage * G::stage(seg);
+            const int s0 = g * seg, cnt = min(seg, a.S - s0);
+            const bool with_live = LIVE && last;
+            float* out = MULTI ? red + (flip * warps + wid) * (seg + 2) : red;
+            for (int r0 = 0; r0 < cnt; r0 += 4) {
+                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (warp_key) {
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int s = min(s0 + r, a.S - 1);
-                const unsigned char* row = a.rows[s] + n * a.row_ld;
-                CacheCodes<BITS> w;
+                    for (int r = 0; r < 4; ++r) {
+                        if (r0 + r >= cnt) break;
+                        uint32_t h[16];
+                        codes(base, r0 + r, h);
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < BITS; ++i) w.w[i] = 0u;
-                sc[r] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < BITS / 4; ++i) {
-                    const uint32_t at = t * (BITS * 4) + i * 16;
-                    if (at < a.codes) {
-                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at));
-                        w.w[4 * i] = u.x, w.w[4 * i + 1] = u.y, w.w[4 * i + 2] = u.z, w.w[4 * i + 3] = u.w;
+                        for (int i = 0; i < 16; i += 2) {
+                            half2_dot(h[i], q[i], d[0], d[1]);
+                            half2_dot(h[i + 1], q[i + 1], d[2], d[3]);
+                        }
+                        p[r] = key ? ((d[0] + d[1]) + (d[2] + d[3])) * back * scale_of(base, r0 + r) : 0.0f;
                     }
                 }
-                if (has) sc[r] = cache_scale(__ldg(row + a.codes + t));
-                const uint2 st = __ldg(reinterpret_cast<const uint2*>(row + a.stat));
-                rs[r] = 1.0f / sqrtf(__uint_as_float(st.x) + a.eps);
-                if (st.y != a.tag) {
-                    if (t == 0 && valid) atomicCAS(&g_cached_fwd_error, 0u, kSiteCacheTag);
-                    rs[r] = __uint_as_float(0x7fc00000u);
-                }
-                w.unpack(h[r]);
-                float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) half2_dot(h[r][i], q[i], d0, d1);
-                p[r] = key ? (d0 + d1) * back * sc[r] : 0.0f;
+                lanes_sum4<LW>(p, out + r0, cnt - r0);
             }
-            team_sum<RB, LW, MULTI>(p, red[flip], warps);
-            flip ^= 1;
-            float mnew = mx;
+            if (with_live) {
+                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (key) {
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                p[r] = s0 + r < a.S ? a.scale * rs[r] * p[r] : __uint_as_float(0xff800000u);
-                mnew = fmaxf(mnew, p[r]);
+                    for (int i = 0; i < 32; ++i) {
+                        const int j = c0 + i - a.ko;
+                        if (j >= 0 && j < a.R) {
+                            const uint32_t w = u4_get(lv[i / 8], i / 2 % 4);
+                            const float v = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+                            p[0] += v * bf16_bits_to_float(__ldg(a.q + j));
+                            p[1] += v * v;
+                        }
+                    }
+                }
+                lanes_sum4<LW>(p, out + cnt, 2);
+            }
+            if constexpr (MULTI) __syncthreads();
+            else __syncwarp();
+            // logits and weights of the segment, by the lanes of each warp
+            float top = __uint_as_float(0xff800000u);
+            const int all = cnt + (with_live ? 1 : 0);
+            for (int s = l; s < all; s += LW) {
+                float dot = 0.0f, ms = 0.0f;
+                if constexpr (MULTI) {
+                    const float* in = red + flip * warps * (seg + 2) + s;
+                    for (int u = 0; u < warps; ++u) dot += in[u * (seg + 2)];
+                    if (with_live && s == cnt)
+                        for (int u = 0; u < warps; ++u) ms += in[u * (seg + 2) + 1];
+                } else {
+                    dot = red[s];
+                    if (with_live && s == cnt) ms = red[s + 1];
+                }
+                float rs;
+                if (with_live && s == cnt) {
+                    rs = 1.0f / sqrtf(ms / static_cast<float>(a.R) + a.eps);
+                } else {
+                    const uint2 stv = *reinterpret_cast<const uint2*>(mine + stage * G::stage(seg) +
+                                                                      seg * (512 * CH + G::SC) + (s * TW + tw) * 8);
+                    rs = 1.0f / sqrtf(__uint_as_float(stv.x) + a.eps);
+                    if (stv.y != a.tag) {
+                        if (valid) atomicCAS(&g_cached_fwd_error, 0u, static_cast<unsigned>(kSiteCacheTag));
+                        rs = __uint_as_float(0x7fc00000u);
+                    }
+                }
+                const float z = a.scale * rs * dot;
+                coef[s] = z;
+                if (!MULTI || wid == 0) zbuf[s0 + s] = z, zbuf[SL + s0 + s] = rs;
+                top = fmaxf(top, z);
+            }
+            const float mnew = fmaxf(mx, lanes_max<LW>(top));
+            float part = 0.0f;
+            for (int s = l; s < all; s += LW) {
+                const float e = expf(coef[s] - mnew);
+                coef[s] = e;
+                part += e;
             }
             const float corr = expf(mx - mnew);
+            sum = sum * corr + lanes_sum<LW>(part);
             mx = mnew;
-            sum *= corr;
+            __syncwarp();
+            if (g > 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmul2(acc[i], make_float2(corr, corr));
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                if (s0 + r >= a.S) break;
-                if (t == 0) zbuf[2 * (s0 + r)] = p[r], zbuf[2 * (s0 + r) + 1] = rs[r];
-                const float e = expf(p[r] - mnew);
-                sum += e;
-                const float2 ce = make_float2(e * sc[r], e * sc[r]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = ffma2(half2_to_f2(h[r][i]), ce, acc[i]);
+                for (int i = 0; i < 16; ++i) acc[i] = fmul2(acc[i], make_float2(corr, corr));
             }
-        }
-        if (a.live) {
-            const uint16_t* row = a.live + n * a.live_ld + c0;
-            float2 x[16];
-            float p[2] = {0.0f, 0.0f};
+#pragma unroll 2
+            for (int r = 0; r < cnt; ++r) {
+                const float c = coef[r] * scale_of(base, r);
+                uint32_t h[16];
+                codes(base, r, h);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (c0 + 8 * i < a.D) u = __ldg(reinterpret_cast<const uint4*>(row) + i);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[4 * i + k] = bf2_to_f2(u4_get(u, k));
+                for (int i = 0; i < 16; ++i) acc[i] = ffma2(half2_to_f2(h[i]), make_float2(c, c), acc[i]);
             }
-            if (key) {
+            if (with_live) {
+                const float c = coef[cnt];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int j = c0 + i - a.ko;
-                    if (j >= 0 && j < a.R) {
-                        const float v = i & 1 ? x[i / 2].y : x[i / 2].x;
-                        p[0] += v * bf16_bits_to_float(__ldg(a.q + j));
-                        p[1] += v * v;
-                    }
-                }
+                for (int i = 0; i < 16; ++i) acc[i] = ffma2(bf2_to_f2(u4_get(lv[i / 4], i % 4)), make_float2(c, c), acc[i]);
             }
-            team_sum<2, LW, MULTI>(p, red[flip], warps);
+            __syncwarp();  // the stage and the coefficients are free again
+            stage ^= 1;
             flip ^= 1;
-            const float rs = 1.0f / sqrtf(p[1] / static_cast<float>(a.R) + a.eps);
-            const float z = a.scale * rs * p[0];
-            const float mnew = fmaxf(mx, z);
-            const float corr = expf(mx - mnew), e = expf(z - mnew);
-            mx = mnew;
-            sum = sum * corr + e;
-            if (t == 0) zbuf[2 * a.S] = z, zbuf[2 * a.S + 1] = rs;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                acc[i] = ffma2(x[i], make_float2(e, e), fmul2(acc[i], make_float2(corr, corr)));
         }
         const float inv = 1.0f / sum;
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = fmul2(acc[i], make_float2(inv, inv));
         if constexpr (NORM) {
-            float ss[1] = {0.0f};
+            float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ss[0] += acc[i].x * acc[i].x + acc[i].y * acc[i].y;
-            team_sum<1, LW, MULTI>(ss, red[flip], warps);
-            flip ^= 1;
-            const float o_rstd = 1.0f / sqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
+            for (int i = 0; i < 16; ++i) ss = ffma2(acc[i], acc[i], ss);
+            float s1 = lanes_sum<LW>(ss.x + ss.y);
+            if constexpr (MULTI) {
+                float* out = red + flip * warps * (seg + 2);
+                if (lane == 0) out[wid] = s1;
+                __syncthreads();
+                s1 = 0.0f;
+                for (int u = 0; u < warps; ++u) s1 += out[u];
+                flip ^= 1;
+            }
+            const float o_rstd = 1.0f / sqrtf(s1 / static_cast<float>(a.D) + a.eps);
             if (t == 0 && valid) a.o_rstd[n] = o_rstd;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int j = c0 + 2 * i;
-                if (j < a.D) {
-                    acc[i].x *= o_rstd * bf16_bits_to_float(__ldg(a.w_o + j));
-                    acc[i].y *= o_rstd * bf16_bits_to_float(__ldg(a.w_o + j + 1));
+            for (int i = 0; i < 4; ++i) {
+                if (c0 + 8 * i < a.D) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.w_o + c0) + i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[4 * i + k] = fmul2(fmul2(acc[4 * i + k], make_float2(o_rstd, o_rstd)), bf2_to_f2(u4_get(w, k)));
                 }
             }
         }
-        if (MULTI) __syncthreads();
-        else __syncwarp();
         if (valid) {
+            uint16_t* y = a.y + n * a.D + c0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (c0 + 8 * i < a.D)
-                    *reinterpret_cast<uint4*>(a.y + n * a.D + c0 + 8 * i) =
-                        make_uint4(pack_f2(acc[4 * i]), pack_f2(acc[4 * i + 1]), pack_f2(acc[4 * i + 2]),
-                                   pack_f2(acc[4 * i + 3]));
+                    *reinterpret_cast<uint4*>(y + 8 * i) = make_uint4(pack_f2(acc[4 * i]), pack_f2(acc[4 * i + 1]),
+                                                                      pack_f2(acc[4 * i + 2]), pack_f2(acc[4 * i + 3]));
             }
-            for (int s = t; s < SL; s += T) {
-                const float z = zbuf[2 * s];
-                a.logit[n * SL + s] = z;
-                a.rstd[n * SL + s] = zbuf[2 * s + 1];
-                a.alpha[n * SL + s] = expf(z - mx) * inv;
+            if (!MULTI || wid == 0) {
+                for (int s = l; s < SL; s += LW) {
+                    const float z = zbuf[s];
+                    a.logit[n * SL + s] = z;
+                    a.rstd[n * SL + s] = zbuf[SL + s];
+                    a.alpha[n * SL + s] = expf(z - mx) * inv;
+                }
             }
         }
-        if (MULTI) __syncthreads();
-        else __syncwarp();
+        __syncwarp();
     }
 }
 
 template <int BITS, int LW, bool MULTI>
 cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
-    const int block = cached_block(a.D), teams = MULTI ? 1 : block / LW;
-    const long long want = (a.N + teams - 1) / teams, most = static_cast<long long>(sm_count) * (512 / block);
-    const int grid = static_cast<int>(want < most ? want : most);
-    const size_t smem = static_cast<size_t>(teams) * 2 * (a.S + 1) * sizeof(float);
-    auto kern = a.w_o ? cached_fwd_kernel<BITS, LW, MULTI, true> : cached_fwd_kernel<BITS, LW, MULTI, false>;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    using G = Seg<BITS, LW>;
+    const int block = cached_block(a.D), warps = block / 32, SL = a.S + (a.live ? 1 : 0);
+    const int seg = G::rows(a.S), per = MULTI ? 1 : warps * G::TW;
+    size_t smem = static_cast<size_t>(warps) * G::warp(seg);
+    if (MULTI) smem += (2 * warps * (seg + 2) * 4 + 15) & ~15;
+    smem += (static_cast<size_t>(per) * 2 * SL * 4 + 15) & ~size_t(15);
+    smem += static_cast<size_t>(a.S) * 8;
+    auto kern = a.w_o ? (a.live ? cached_fwd_kernel<BITS, LW, MULTI, true, true> : cached_fwd_kernel<BITS, LW, MULTI, true, false>)
+                      : (a.live ? cached_fwd_kernel<BITS, LW, MULTI, false, true> : cached_fwd_kernel<BITS, LW, MULTI, false, false>);
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    return launch_pdl(kern, dim3(grid), dim3(block), smem, stream, a);
+    int fit = 0;
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, block, smem);
+    if (err != cudaSuccess) return err;
+    if (fit < 1) return cudaErrorInvalidConfiguration;
+    const long long want = (a.N + per - 1) / per, most = static_cast<long long>(sm_count) * fit;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(block), smem, stream, a);
 }
 
 template <int BITS>
