@@ -8,6 +8,8 @@
 // block into the FP32 mixture while its half pairs are still in registers.
 // The key statistic of a cached row is read from its record; the live bf16
 // source, read last, gets its own.
+#include <type_traits>
+
 #include "cached.cuh"
 #include "kernels.cuh"
 #include "launch_pdl.cuh"
@@ -94,24 +96,22 @@ __device__ __forceinline__ float lanes_max(float x) {
     return x;
 }
 
-// Sums of four values over the LW lanes of a team; afterwards the team's lane
-// 0 writes them to out[0..3] (only the first `rows`).
-template <int LW>
-__device__ __forceinline__ void lanes_sum4(float (&p)[4], float* out, int rows) {
+// Sums of K (1, 2 or 4) values over the LW lanes of a team, written to out[0..K).
+template <int LW, int K>
+__device__ __forceinline__ void lanes_sum_to(float (&p)[K], float* out) {
     const int lane = threadIdx.x & 31;
-    if constexpr (LW == 32) {  // one lane in eight ends up with one of the sums
-        warp_reduce_scatter<4>(p, lane);
-        if ((lane & 7) == 0 && (lane >> 3) < rows) out[lane >> 3] = p[0];
+    if constexpr (LW == 32) {  // one lane in 32 / K ends up with one of the sums
+        warp_reduce_scatter<K>(p, lane);
+        if ((lane & (32 / K - 1)) == 0) out[lane / (32 / K)] = p[0];
     } else {
 #pragma unroll
         for (int o = LW / 2; o > 0; o >>= 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] += __shfl_xor_sync(0xffffffffu, p[i], o);
+            for (int i = 0; i < K; ++i) p[i] += __shfl_xor_sync(0xffffffffu, p[i], o);
         }
         if (lane % LW == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < rows) out[i] = p[i];
+            for (int i = 0; i < K; ++i) out[i] = p[i];
         }
     }
 }
@@ -201,20 +201,50 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
         }
         cp_async_commit();
     };
-    auto codes = [&](uint32_t base, int r, uint32_t (&h)[16]) {
+    // this thread's codes and scale byte of a segment's row 0
+    uint32_t code_at[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = lane * CH + i;
+        code_at[i] = (CH == 2 ? c ^ ((c >> 3) & 1) : c) * 16;
+    }
+    const uint32_t scale_at = seg * 512 * CH + (LW >= 8 ? lane : tw * 8 + l);
+    auto codes = [&](uint32_t base, int r) {
         CacheCodes<BITS> w;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = lane * CH + i;
-            const uint4 u = lds128(base + r * 512 * CH + (CH == 2 ? c ^ ((c >> 3) & 1) : c) * 16);
+            const uint4 u = lds128(base + code_at[i] + r * 512 * CH);
             w.w[4 * i] = u.x, w.w[4 * i + 1] = u.y, w.w[4 * i + 2] = u.z, w.w[4 * i + 3] = u.w;
         }
-        w.unpack(h);
+        return w;
     };
+    // a thread without channels reads some other byte: its codes are zero and its sums unused
     auto scale_of = [&](uint32_t base, int r) {
         uint32_t b;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(base + seg * 512 * CH + r * G::SC + (LW >= 8 ? lane : tw * 8 + l)));
-        return has ? cache_scale(b) : 0.0f;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(base + scale_at + r * G::SC));
+        return cache_scale(b);
+    };
+    // dots of rows r0 .. r0 + K - 1 with the query, summed over the team's lanes of this warp
+    auto dots = [&](auto count, uint32_t base, int r0, float* out) {
+        constexpr int K = decltype(count)::value;
+        float p[K];
+        CacheCodes<BITS> w[K];
+        float sc[K];
+#pragma unroll
+        for (int r = 0; r < K; ++r) w[r] = codes(base, r0 + r), sc[r] = scale_of(base, r0 + r);
+#pragma unroll
+        for (int r = 0; r < K; ++r) {
+            uint32_t h[16];
+            w[r].unpack(h);
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                half2_dot(h[i], q[i], d[0], d[1]);
+                half2_dot(h[i + 1], q[i + 1], d[2], d[3]);
+            }
+            p[r] = key ? ((d[0] + d[1]) + (d[2] + d[3])) * back * sc[r] : 0.0f;
+        }
+        lanes_sum_to<LW>(p, out + r0);
     };
 
     issue(0, first, 0);
@@ -247,27 +277,16 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
             const int s0 = g * seg, cnt = min(seg, a.S - s0);
             const bool with_live = LIVE && last;
             float* out = MULTI ? red + (flip * warps + wid) * (seg + 2) : red;
-            for (int r0 = 0; r0 < cnt; r0 += 4) {
-                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (warp_key) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (r0 + r >= cnt) break;
-                        uint32_t h[16];
-                        codes(base, r0 + r, h);
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            half2_dot(h[i], q[i], d[0], d[1]);
-                            half2_dot(h[i + 1], q[i + 1], d[2], d[3]);
-                        }
-                        p[r] = key ? ((d[0] + d[1]) + (d[2] + d[3])) * back * scale_of(base, r0 + r) : 0.0f;
-                    }
-                }
-                lanes_sum4<LW>(p, out + r0, cnt - r0);
+            if (warp_key) {
+                int r = 0;
+                for (; r + 4 <= cnt; r += 4) dots(std::integral_constant<int, 4>{}, base, r, out);
+                if (cnt & 2) dots(std::integral_constant<int, 2>{}, base, r, out), r += 2;
+                if (cnt & 1) dots(std::integral_constant<int, 1>{}, base, r, out);
+            } else {
+                for (int r = l; r < cnt; r += LW) out[r] = 0.0f;
             }
             if (with_live) {
-                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                float p[2] = {0.0f, 0.0f};
                 if (key) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
                         }
                     }
                 }
-                lanes_sum4<LW>(p, out + cnt, 2);
+                lanes_sum_to<LW>(p, out + cnt);
             }
             if constexpr (MULTI) __syncthreads();
             else __syncwarp();
@@ -300,11 +319,11 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
                 }
                 float rs;
                 if (with_live && s == cnt) {
-                    rs = 1.0f / sqrtf(ms / static_cast<float>(a.R) + a.eps);
+                    rs = rsqrtf(ms / static_cast<float>(a.R) + a.eps);
                 } else {
                     const uint2 stv = *reinterpret_cast<const uint2*>(mine + stage * G::stage(seg) +
                                                                       seg * (512 * CH + G::SC) + (s * TW + tw) * 8);
-                    rs = 1.0f / sqrtf(__uint_as_float(stv.x) + a.eps);
+                    rs = rsqrtf(__uint_as_float(stv.x) + a.eps);
                     if (stv.y != a.tag) {
                         if (valid) atomicCAS(&g_cached_fwd_error, 0u, static_cast<unsigned>(kSiteCacheTag));
                         rs = __uint_as_float(0x7fc00000u);
@@ -330,13 +349,25 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i] = fmul2(acc[i], make_float2(corr, corr));
             }
-#pragma unroll 2
-            for (int r = 0; r < cnt; ++r) {
-                const float c = coef[r] * scale_of(base, r);
-                uint32_t h[16];
-                codes(base, r, h);
+            auto mix = [&](auto count, int r0) {
+                constexpr int K = decltype(count)::value;
+                CacheCodes<BITS> w[K];
+                float c[K];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = ffma2(half2_to_f2(h[i]), make_float2(c, c), acc[i]);
+                for (int r = 0; r < K; ++r) w[r] = codes(base, r0 + r), c[r] = coef[r0 + r] * scale_of(base, r0 + r);
+#pragma unroll
+                for (int r = 0; r < K; ++r) {
+                    uint32_t h[16];
+                    w[r].unpack(h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[i] = ffma2(half2_to_f2(h[i]), make_float2(c[r], c[r]), acc[i]);
+                }
+            };
+            {
+                int r = 0;
+                for (; r + 4 <= cnt; r += 4) mix(std::integral_constant<int, 4>{}, r);
+                if (cnt & 2) mix(std::integral_constant<int, 2>{}, r), r += 2;
+                if (cnt & 1) mix(std::integral_constant<int, 1>{}, r);
             }
             if (with_live) {
                 const float c = coef[cnt];
@@ -348,13 +379,12 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
             flip ^= 1;
         }
         const float inv = 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = fmul2(acc[i], make_float2(inv, inv));
+        float2 out2 = make_float2(inv, inv);
         if constexpr (NORM) {
             float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < 16; ++i) ss = ffma2(acc[i], acc[i], ss);
-            float s1 = lanes_sum<LW>(ss.x + ss.y);
+            float s1 = lanes_sum<LW>(has ? ss.x + ss.y : 0.0f);
             if constexpr (MULTI) {
                 float* out = red + flip * warps * (seg + 2);
                 if (lane == 0) out[wid] = s1;
@@ -363,16 +393,19 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
                 for (int u = 0; u < warps; ++u) s1 += out[u];
                 flip ^= 1;
             }
-            const float o_rstd = 1.0f / sqrtf(s1 / static_cast<float>(a.D) + a.eps);
+            const float o_rstd = rsqrtf(s1 * inv * inv / static_cast<float>(a.D) + a.eps);
             if (t == 0 && valid) a.o_rstd[n] = o_rstd;
+            out2 = make_float2(inv * o_rstd, inv * o_rstd);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (c0 + 8 * i < a.D) {
-                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.w_o + c0) + i);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (NORM) {
+                const uint4 w = c0 + 8 * i < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + c0) + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[4 * i + k] = fmul2(fmul2(acc[4 * i + k], make_float2(o_rstd, o_rstd)), bf2_to_f2(u4_get(w, k)));
-                }
+                for (int k = 0; k < 4; ++k) acc[4 * i + k] = fmul2(fmul2(acc[4 * i + k], out2), bf2_to_f2(u4_get(w, k)));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[4 * i + k] = fmul2(acc[4 * i + k], out2);
             }
         }
         if (valid) {
