@@ -133,11 +133,11 @@ __global__ void __launch_bounds__(256) cache_load_kernel(const CacheRowsArgs a) 
             up = __uint_as_float(0x7fc00000u);
         }
         uint4 o;
-        const float2 s = make_float2(up, up);
-        o.x = pack_f2(fmul2(half2_to_f2(h[0]), s));
-        o.y = pack_f2(fmul2(half2_to_f2(h[1]), s));
-        o.z = pack_f2(fmul2(half2_to_f2(h[2]), s));
-        o.w = pack_f2(fmul2(half2_to_f2(h[3]), s));
+        const f2 s = f2_dup(up);
+        o.x = f2_to_bf16(f2_mul(f2_half(h[0]), s));
+        o.y = f2_to_bf16(f2_mul(f2_half(h[1]), s));
+        o.z = f2_to_bf16(f2_mul(f2_half(h[2]), s));
+        o.w = f2_to_bf16(f2_mul(f2_half(h[3]), s));
         *reinterpret_cast<uint4*>(a.out + n * a.x_ld + c) = o;
     }
 }

@@ -178,7 +178,7 @@ size_t attnres_cached_bwd_workspace_bytes(const attnres_cached_params* p) {
     if (check_cached(p) != ATTNRES_OK || p->N == 0) return 0;
     const int sms = sm_count();
     if (!sms) return 0;
-    return static_cast<size_t>(cached_bwd_grid(p->N, p->D, sms)) * (p->R + (p->out_norm ? p->D : 0)) * sizeof(float);
+    return static_cast<size_t>(cached_bwd_grid(p->S, p->live != nullptr, p->N, p->D, p->bits, sms)) * (p->R + (p->out_norm ? p->D : 0)) * sizeof(float);
 }
 
 attnres_status attnres_cached_bwd(const attnres_cached_params* p, const void* q, const void* w_o, const void* dy,
@@ -227,7 +227,7 @@ attnres_status attnres_cached_bwd(const attnres_cached_params* p, const void* q,
     }
     const int sms = sm_count();
     if (!sms) return ATTNRES_ERR_CUDA;
-    const int grid = cached_bwd_grid(p->N, p->D, sms);
+    const int grid = cached_bwd_grid(p->S, p->live != nullptr, p->N, p->D, p->bits, sms);
     const int W = p->R + (p->out_norm ? p->D : 0);
     if (!workspace || workspace_bytes < static_cast<size_t>(grid) * W * sizeof(float)) return ATTNRES_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return ATTNRES_ERR_ALIGNMENT;
@@ -241,11 +241,14 @@ attnres_status attnres_cached_bwd(const attnres_cached_params* p, const void* q,
     b.want_dsrc = dsrc != nullptr;
     for (int i = 0; dsrc && i < p->S; ++i) b.dsrc[i] = static_cast<uint16_t*>(dsrc[i]);
     b.dsrc_ld = dsrc_ld;
+    b.wide_src = p->D % 16 == 0 && dsrc_ld % 16 == 0;
+    for (int i = 0; dsrc && i < p->S; ++i) b.wide_src = b.wide_src && aligned(dsrc[i], 32);
+    b.wide_live = p->D % 16 == 0 && dlive_ld % 16 == 0 && aligned(dlive, 32);
     b.dlive = static_cast<uint16_t*>(dlive);
     b.dlive_ld = dlive_ld;
     b.dy = static_cast<const uint16_t*>(dy);
     b.part = static_cast<float*>(workspace);
-    if (launch_cached_bwd(b, p->bits, grid, s) != cudaSuccess) return ATTNRES_ERR_CUDA;
+    if (launch_cached_bwd(b, p->bits, grid, sms, s) != cudaSuccess) return ATTNRES_ERR_CUDA;
     return launch_finalize(b.part, grid, p->R, W, static_cast<uint16_t*>(dq), dq_f32, static_cast<uint16_t*>(dw_o),
                            dw_o_f32, s) == cudaSuccess
                ? ATTNRES_OK

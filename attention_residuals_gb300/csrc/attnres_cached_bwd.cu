@@ -7,232 +7,404 @@
 //   dv_s  = a_s * do + [key] (scale dz_s r_s q - dz_s z_s r_s^2 / R * t_s)
 //   dq    = sum over tokens and sources of scale dz_s r_s t_s
 //   dw_o  = sum over tokens of dy * o * o_rstd
-// A team of threads shares a token, one thread per 32 channels.  The rows are
-// read once per pass (the mixture o when there is an output norm, the dots,
-// the gradients); after the first they come from L2.  dq and dw_o are FP32
-// sums in registers over the CTA's tokens, one partial row per CTA, added in
-// a fixed order by the finalize kernel.
-#include "cached.cuh"
+// A team of threads shares a token, one thread per 32 channels; three passes
+// over its rows form o (with an output norm), the dots da and the gradients.
+// Raw rows, dy and the statistics of the next step are copied to the warp's
+// shared memory while one is worked on: whole tokens where two of them fit,
+// so that a row is read once, else segments of rows per pass, which after the
+// first pass come from L2.  dq and dw_o are summed in registers over the CTA's
+// tokens; each CTA writes one partial row and the finalize kernel adds the
+// rows in a fixed order.
+#include <type_traits>
+
+#include "cached_stage.cuh"
 #include "kernels.cuh"
 #include "launch_pdl.cuh"
 
 namespace attnres {
 namespace {
 
-__device__ unsigned g_cached_bwd_error;
+constexpr int kBwdThreads = 256;      // threads of an SM (up to 255 registers each)
+constexpr int kSmemSm = 227 * 1024;   // shared memory of an SM that CTAs can have
+constexpr int kResidentWarp = 28 << 10;  // a warp's shared memory up to which whole tokens are kept (8 warps of an SM)
+constexpr int kStreamWarp = 18 << 10;    // its target where tokens are streamed (12 warps)
 
-constexpr int RB = 4;
+// Shared memory of a warp, in this order: two stages of rows, two of the
+// tokens' bf16 rows and statistics, the dots unless they are the CTA's.
+template <int BITS, int LW, bool MULTI>
+struct Bwd : RowStage<BITS, LW, MULTI> {
+    using R = RowStage<BITS, LW, MULTI>;
+    __host__ __device__ static int stats(int SL) { return (3 * SL * R::TW * 4 + 15) & ~15; }
+    __host__ __device__ static int token(int SL, bool live) { return R::BF16 * (live ? 2 : 1) + stats(SL); }
+    __host__ __device__ static int dots(int SL) { return MULTI ? 0 : (SL * R::TW * 4 + 15) & ~15; }
+    __host__ __device__ static int fixed(int SL, bool live) {
+        return 2 * token(SL, live) + dots(SL);
+    }
+    __host__ __device__ static int warp(int seg, int SL, bool live) {
+        return 2 * R::bytes(seg) + fixed(SL, live);
+    }
+    // of the CTA, behind the warps': dots in two buffers used in turn, <h, o>, the sources' addresses
+    __host__ __device__ static int cta(int warps, int S, int SL) {
+        return (MULTI ? (2 * warps * (SL + 1) * 4 + 15) & ~15 : 0) + S * 8;
+    }
+};
 
-template <int K, int LW, bool MULTI>
-__device__ __forceinline__ void team_sum(float (&v)[K], float* red, int warps) {
-#pragma unroll
-    for (int o = LW / 2; o > 0; o >>= 1) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+struct BwdPlan {
+    int block, seg, fit, grid;
+    size_t smem;
+};
+
+template <int BITS, int LW, bool MULTI>
+BwdPlan plan_t(int S, bool live, long long N, int D, int sm_count) {
+    using G = Bwd<BITS, LW, MULTI>;
+    const int SL = S + (live ? 1 : 0), fixed = G::fixed(SL, live);
+    BwdPlan p{};
+    p.seg = S;
+    if (G::warp(S, SL, live) > kResidentWarp) {
+        int most = (kStreamWarp - fixed) / (2 * G::ROW);
+        if (most < 4) most = 4;
+        const int n = (S + most - 1) / most;
+        p.seg = (S + n - 1) / n;
     }
-    if constexpr (MULTI) {
-        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) red[w * K + i] = v[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < K; ++i) v[i] = 0.0f;
-        for (int u = 0; u < warps; ++u) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) v[i] += red[u * K + i];
-        }
+    p.block = cached_block(D);
+    for (;;) {
+        const int warps = p.block / 32;
+        p.smem = static_cast<size_t>(warps) * G::warp(p.seg, SL, live) + G::cta(warps, S, SL);
+        if (MULTI || p.block == 32 || p.smem <= kSmemSm / 2) break;
+        p.block /= 2;
     }
+    int by_smem = static_cast<int>(kSmemSm / (p.smem + 1024)), by_regs = kBwdThreads / p.block;
+    p.fit = by_smem < by_regs ? by_smem : by_regs;
+    if (p.fit < 1) p.fit = 1;
+    const long long per = MULTI ? 1 : p.block / 32 * G::TW;
+    const long long want = (N + per - 1) / per, most = static_cast<long long>(sm_count) * p.fit;
+    p.grid = static_cast<int>(want < most ? want : most);
+    return p;
 }
 
-// One row's 32 channels of this thread: half pairs and their scale.
-template <int BITS>
-__device__ __forceinline__ float load_row(const CachedArgs& a, int s, long long n, int t, bool has, uint32_t (&h)[16]) {
-    const unsigned char* row = a.rows[s] + n * a.row_ld;
-    CacheCodes<BITS> w;
-#pragma unroll
-    for (int i = 0; i < BITS; ++i) w.w[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < BITS / 4; ++i) {
-        const uint32_t at = t * (BITS * 4) + i * 16;
-        if (at < a.codes) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at));
-            w.w[4 * i] = u.x, w.w[4 * i + 1] = u.y, w.w[4 * i + 2] = u.z, w.w[4 * i + 3] = u.w;
-        }
-    }
-    w.unpack(h);
-    return has ? cache_scale(__ldg(row + a.codes + t)) : 0.0f;
-}
-
-__device__ __forceinline__ void load_bf16(const uint16_t* p, int c0, int D, float2 (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (c0 + 8 * i < D) u = __ldg(reinterpret_cast<const uint4*>(p + c0) + i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[4 * i + k] = bf2_to_f2(u4_get(u, k));
-    }
-}
-
-__device__ __forceinline__ void store_bf16(uint16_t* p, int c0, int D, const float2 (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (c0 + 8 * i < D)
-            *reinterpret_cast<uint4*>(p + c0 + 8 * i) = make_uint4(pack_f2(x[4 * i]), pack_f2(x[4 * i + 1]),
-                                                                   pack_f2(x[4 * i + 2]), pack_f2(x[4 * i + 3]));
-    }
-}
-
-template <int BITS, int LW, bool MULTI, bool NORM>
-__global__ void __launch_bounds__(256) cached_bwd_kernel(const CachedBwdArgs b) {
-    __shared__ float red[2][8 * RB];
-    extern __shared__ float dyn[];
+template <int BITS, int LW, bool MULTI, bool NORM, bool LIVE>
+__global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const CachedBwdArgs b) {
+    using G = Bwd<BITS, LW, MULTI>;
+    constexpr int CH = G::CH, TW = G::TW;
+    extern __shared__ __align__(16) unsigned char dyn[];
     const CachedArgs& a = b.c;
     pdl_wait();
-    const int warps = blockDim.x >> 5;
-    const int T = MULTI ? blockDim.x : LW;
-    const int teams = MULTI ? 1 : blockDim.x / LW;
-    const int team = MULTI ? 0 : threadIdx.x / LW, t = MULTI ? threadIdx.x : threadIdx.x % LW;
-    const int c0 = t * 32;
-    const int SL = a.S + (a.live ? 1 : 0);
-    float* da = dyn + team * SL;  // the token's <do, v_s>
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int l = lane % LW, tw = lane / LW;
+    const int t = MULTI ? threadIdx.x : l, c0 = t * 32;
+    const int SL = a.S + (LIVE ? 1 : 0);
+    const int seg = b.seg, nseg = (a.S + seg - 1) / seg;
+    const bool resident = nseg == 1;
+    const int warp_bytes = G::warp(seg, SL, LIVE);
+    unsigned char* mine = dyn + wid * warp_bytes;
+    const uint32_t st0 = smem_u32(mine);
+    const int tok_at = 2 * G::bytes(seg), tok_bytes = G::token(SL, LIVE);
+    unsigned char* rest = dyn + warps * warp_bytes;
+    float* red = MULTI ? reinterpret_cast<float*>(rest)
+                       : reinterpret_cast<float*>(mine + tok_at + 2 * tok_bytes) + tw * SL;
+    float* ho_red = red + 2 * warps * SL;  // MULTI
+    if (MULTI) rest += (2 * warps * (SL + 1) * 4 + 15) & ~15;
+    const unsigned char** rows = reinterpret_cast<const unsigned char**>(rest);
+    for (int s = threadIdx.x; s < a.S; s += blockDim.x) rows[s] = a.rows[s];
     const bool has = c0 < a.D, key = has && c0 < a.ko + a.R && c0 + 32 > a.ko;
-    float2 q[16], dq[16], dw[16];
+    const bool warp_key = __any_sync(0xffffffffu, key);
+    f2 q[16], dq[16], dw[16];
+    uint32_t mask = 0;  // bit i: channel c0 + i is a key channel
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int j = c0 + 2 * i - a.ko;
-        q[i].x = j >= 0 && j < a.R ? bf16_bits_to_float(__ldg(a.q + j)) : 0.0f;
-        q[i].y = j + 1 >= 0 && j + 1 < a.R ? bf16_bits_to_float(__ldg(a.q + j + 1)) : 0.0f;
-        dq[i] = dw[i] = make_float2(0.0f, 0.0f);
+        const bool x = j >= 0 && j < a.R, y = j + 1 >= 0 && j + 1 < a.R;
+        q[i] = f2_make(x ? bf16_bits_to_float(__ldg(a.q + j)) : 0.0f, y ? bf16_bits_to_float(__ldg(a.q + j + 1)) : 0.0f);
+        mask |= (x ? 1u : 0u) << (2 * i) | (y ? 1u : 0u) << (2 * i + 1);
+        dq[i] = dw[i] = 0ull;
     }
-    // bit i: channel c0 + i is a key channel
-    uint32_t mask = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (c0 + i >= a.ko && c0 + i < a.ko + a.R) mask |= 1u << i;
-    int flip = 0;
-    const long long stride = static_cast<long long>(gridDim.x) * teams;
-    for (long long base = static_cast<long long>(blockIdx.x) * teams; base < a.N; base += stride) {
-        const bool valid = base + team < a.N;
-        const long long n = valid ? base + team : a.N - 1;
-        const float* al = a.alpha + n * SL;
-        const float* rs = a.rstd + n * SL;
-        const float* lg = a.logit + n * SL;
-        float2 g[16];  // do
-        load_bf16(b.dy + n * a.D, c0, a.D, g);
-        if constexpr (NORM) {
-            float2 o[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = make_float2(0.0f, 0.0f);
-            for (int s = 0; s < a.S; ++s) {
-                uint32_t h[16];
-                const float sc = load_row<BITS>(a, s, n, t, has, h) * al[s];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = ffma2(half2_to_f2(h[i]), make_float2(sc, sc), o[i]);
-            }
-            if (a.live) {
-                float2 x[16];
-                load_bf16(a.live + n * a.live_ld, c0, a.D, x);
-                const float al_s = al[a.S];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = ffma2(x[i], make_float2(al_s, al_s), o[i]);
-            }
-            const float r = a.o_rstd[n];
-            float2 w[16];
-            load_bf16(a.w_o, c0, a.D, w);
-            float ho[1] = {0.0f};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (valid) dw[i] = ffma2(g[i], fmul2(o[i], make_float2(r, r)), dw[i]);
-                g[i] = fmul2(g[i], w[i]);
-                ho[0] += g[i].x * o[i].x + g[i].y * o[i].y;
-            }
-            team_sum<1, LW, MULTI>(ho, red[flip], warps);
-            flip ^= 1;
-            const float c = -r * r * ho[0] / static_cast<float>(a.D);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = fmul2(ffma2(o[i], make_float2(c, c), g[i]), make_float2(r, r));
+    const bool ragged = __any_sync(0xffffffffu, mask != 0xffffffffu);
+    __syncthreads();
+    uint32_t code_at[CH], scale_at;
+    G::places(seg, code_at, scale_at);
+    const float inv_D = 1.0f / static_cast<float>(a.D), inv_R = 1.0f / static_cast<float>(a.R);
+
+    const int per = MULTI ? 1 : warps * TW;
+    const long long stride = static_cast<long long>(gridDim.x) * per;
+    const long long first = static_cast<long long>(blockIdx.x) * per + (MULTI ? 0 : wid * TW);
+    auto copy_rows = [&](int stage, long long n0, int g) {
+        G::copy(a, rows, st0 + stage * G::bytes(seg), seg, n0, g * seg, min(seg, a.S - g * seg));
+    };
+    auto copy_token = [&](int tb, long long n0) {
+        const uint32_t at = st0 + tok_at + tb * tok_bytes;
+        G::copy_bf16(b.dy, a.D, at, n0, a.N, a.D);
+        if constexpr (LIVE) G::copy_bf16(a.live, a.live_ld, at + G::BF16, n0, a.N, a.D);
+        const uint32_t st = at + G::BF16 * (LIVE ? 2 : 1);
+        for (int i = lane; i < TW * SL; i += 32) {
+            const long long from = TW == 1 ? n0 * SL + i : min(n0 + i / SL, a.N - 1) * SL + i % SL;
+            cp_async_4s(st + i * 4, a.alpha + from);
+            cp_async_4s(st + (TW * SL + i) * 4, a.rstd + from);
+            cp_async_4s(st + (2 * TW * SL + i) * 4, a.logit + from);
         }
-        for (int s0 = 0; s0 < SL; s0 += RB) {
-            float p[RB];
+    };
+    constexpr int kFirst = NORM ? 0 : 1;
+    int stage = 0, tb = 0, flip = 0;
+    if (first < a.N) {
+        copy_token(0, first);
+        copy_rows(0, first, 0);
+        cp_async_commit();
+    }
+    for (long long n0 = first; n0 < a.N; n0 += stride) {
+        const bool valid = n0 + tw < a.N;
+        const long long n = valid ? n0 + tw : a.N - 1;
+        const bool more = n0 + stride < a.N;
+        const uint32_t tok = st0 + tok_at + tb * tok_bytes;
+        // alpha, then 1 / RMS and logit, which become the coefficients of q and of t
+        float* al = reinterpret_cast<float*>(mine + tok_at + tb * tok_bytes + G::BF16 * (LIVE ? 2 : 1)) + tw * SL;
+        float* k1 = al + TW * SL;
+        float* k2 = k1 + TW * SL;
+        f2 g[16];  // do
+        auto load_g = [&](uint32_t at) {
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int s = s0 + r;
-                p[r] = 0.0f;
-                if (s < a.S) {
-                    uint32_t h[16];
-                    const float sc = load_row<BITS>(a, s, n, t, has, h);
-                    float2 d = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 u = G::bf16_part(at, i);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) d = ffma2(half2_to_f2(h[i]), g[i], d);
-                    if (has) p[r] = (d.x + d.y) * sc;
-                } else if (s == a.S && a.live) {
-                    float2 x[16];
-                    load_bf16(a.live + n * a.live_ld, c0, a.D, x);
-                    float2 d = make_float2(0.0f, 0.0f);
+                for (int k = 0; k < 4; ++k) g[4 * i + k] = f2_bf16(u4_get(u, k));
+            }
+        };
+        // makes the rows of (pass, segment) ready and starts the copies of what comes next
+        auto next = [&](int pass, int seg_i) {
+            if (resident) {
+                if (pass != kFirst) return;
+                if (more) {
+                    copy_token(tb ^ 1, n0 + stride);
+                    copy_rows(stage ^ 1, n0 + stride, 0);
+                }
+            } else if (seg_i < nseg - 1 || pass < 2) {
+                copy_rows(stage ^ 1, n0, seg_i < nseg - 1 ? seg_i + 1 : 0);
+            } else if (more) {
+                copy_token(tb ^ 1, n0 + stride);
+                copy_rows(stage ^ 1, n0 + stride, 0);
+            }
+            cp_async_commit();
+            cp_async_wait<1>();
+            __syncwarp();
+        };
+        auto done = [&](int pass, int seg_i) {
+            __syncwarp();
+            if (!resident || pass == 2) stage ^= 1;
+        };
+        if constexpr (NORM) {
+            f2 o[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) d = ffma2(x[i], g[i], d);
-                    p[r] = d.x + d.y;
+            for (int i = 0; i < 16; ++i) o[i] = 0ull;
+            for (int u = 0; u < nseg; ++u) {
+                next(0, u);
+                const uint32_t base = st0 + stage * G::bytes(seg);
+                const int s0 = u * seg, cnt = min(seg, a.S - s0);
+                auto mix = [&](auto count, int r0) {
+                    constexpr int K = decltype(count)::value;
+                    CacheCodes<BITS> w[K];
+                    float c[K];
+#pragma unroll
+                    for (int r = 0; r < K; ++r)
+                        w[r] = G::codes(base, code_at, r0 + r), c[r] = al[s0 + r0 + r] * G::scale(base, scale_at, r0 + r);
+#pragma unroll
+                    for (int r = 0; r < K; ++r) {
+                        uint32_t h[16];
+                        w[r].unpack(h);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = f2_fma(f2_half(h[i]), f2_dup(c[r]), o[i]);
+                    }
+                };
+                int r = 0;
+                for (; r + 2 <= cnt; r += 2) mix(std::integral_constant<int, 2>{}, r);
+                if (r < cnt) mix(std::integral_constant<int, 1>{}, r);
+                done(0, u);
+            }
+            if constexpr (LIVE) {
+                const float c = al[a.S];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 x = G::bf16_part(tok + G::BF16, i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[4 * i + k] = f2_fma(f2_bf16(u4_get(x, k)), f2_dup(c), o[4 * i + k]);
                 }
             }
-            team_sum<RB, LW, MULTI>(p, red[flip], warps);
-            flip ^= 1;
-            if (t == 0) {
+            load_g(tok);
+            const float r = a.o_rstd[n];
+            f2 s2 = 0ull;
+            if (has) {
 #pragma unroll
-                for (int r = 0; r < RB; ++r)
-                    if (s0 + r < SL) da[s0 + r] = p[r];
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w = c0 + 8 * i < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + c0) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = 4 * i + k;
+                        if (valid) dw[j] = f2_fma(g[j], f2_mul(o[j], f2_dup(r)), dw[j]);
+                        g[j] = f2_mul(g[j], f2_bf16(u4_get(w, k)));
+                        s2 = f2_fma(g[j], o[j], s2);
+                    }
+                }
+            }
+            float ho = lanes_sum<LW>(f2_sum(s2));
+            if constexpr (MULTI) {
+                float* out = ho_red + flip * warps;
+                if (lane == 0) out[wid] = ho;
+                __syncthreads();
+                ho = 0.0f;
+                for (int u = 0; u < warps; ++u) ho += out[u];
+            }
+            const float c = -r * r * ho * inv_D;
+            if (has) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] = f2_mul(f2_fma(o[i], f2_dup(c), g[i]), f2_dup(r));
             }
         }
-        if (MULTI) __syncthreads();
+        float* out = MULTI ? red + (flip * warps + wid) * SL : red;
+        for (int u = 0; u < nseg; ++u) {
+            next(1, u);
+            if (!NORM && u == 0) load_g(tok);
+            const uint32_t base = st0 + stage * G::bytes(seg);
+            const int s0 = u * seg, cnt = min(seg, a.S - s0);
+            auto dots = [&](auto count, int r0) {
+                constexpr int K = decltype(count)::value;
+                CacheCodes<BITS> w[K];
+                float sc[K], p[K];
+#pragma unroll
+                for (int r = 0; r < K; ++r) w[r] = G::codes(base, code_at, r0 + r), sc[r] = G::scale(base, scale_at, r0 + r);
+#pragma unroll
+                for (int r = 0; r < K; ++r) {
+                    uint32_t h[16];
+                    w[r].unpack(h);
+                    f2 d0 = 0ull, d1 = d0;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        d0 = f2_fma(f2_half(h[i]), g[i], d0);
+                        d1 = f2_fma(f2_half(h[i + 1]), g[i + 1], d1);
+                    }
+                    p[r] = has ? (f2_sum(d0) + f2_sum(d1)) * sc[r] : 0.0f;
+                }
+                lanes_sum_to<LW>(p, out + s0 + r0);
+            };
+            int r = 0;
+            for (; r + 4 <= cnt; r += 4) dots(std::integral_constant<int, 4>{}, r);
+            if (cnt & 2) dots(std::integral_constant<int, 2>{}, r), r += 2;
+            if (cnt & 1) dots(std::integral_constant<int, 1>{}, r);
+            done(1, u);
+        }
+        if constexpr (LIVE) {
+            f2 d = 0ull;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 x = G::bf16_part(tok + G::BF16, i);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d = f2_fma(f2_bf16(u4_get(x, k)), g[4 * i + k], d);
+            }
+            float p[1] = {f2_sum(d)};
+            lanes_sum_to<LW>(p, out + a.S);
+        }
+        if constexpr (MULTI) __syncthreads();
         else __syncwarp();
         float mean = 0.0f;  // sum_u a_u da_u
-        for (int s = 0; s < SL; ++s) mean += al[s] * da[s];
-        for (int s = 0; s < SL; ++s) {
-            const float as = al[s];
-            const float dz = as * (da[s] - mean);
-            const float k1 = a.scale * dz * rs[s], k2 = -dz * lg[s] * rs[s] * rs[s] / static_cast<float>(a.R);
-            const bool is_live = s == a.S;
-            uint16_t* out = is_live ? b.dlive : (b.want_dsrc ? b.dsrc[s] : nullptr);
-            const long long ld = is_live ? b.dlive_ld : b.dsrc_ld;
-            float2 d[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) d[i] = fmul2(g[i], make_float2(as, as));
-            if (key) {
-                float2 x[16];
-                if (is_live) {
-                    load_bf16(a.live + n * a.live_ld, c0, a.D, x);
-                } else {
-                    uint32_t h[16];
-                    const float sc = load_row<BITS>(a, s, n, t, has, h);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = fmul2(half2_to_f2(h[i]), make_float2(sc, sc));
-                }
+        for (int s = l; s < SL; s += LW) {
+            float d = 0.0f;
+            if constexpr (MULTI) {
+                for (int u = 0; u < warps; ++u) d += red[(flip * warps + u) * SL + s];
+            } else {
+                d = red[s];
+            }
+            const float as = al[s], rs = k1[s];
+            mean += as * d;
+            k2[s] = -k2[s] * rs * rs * inv_R;  // for dz
+            k1[s] = a.scale * rs;
+            if constexpr (!MULTI) red[s] = d;
+        }
+        mean = lanes_sum<LW>(mean);
+        for (int s = l; s < SL; s += LW) {
+            float d = 0.0f;
+            if constexpr (MULTI) {
+                for (int u = 0; u < warps; ++u) d += red[(flip * warps + u) * SL + s];
+            } else {
+                d = red[s];
+            }
+            const float dz = al[s] * (d - mean);
+            k1[s] *= dz;
+            k2[s] *= dz;
+        }
+        flip ^= 1;
+        __syncwarp();
+        for (int u = 0; u < nseg; ++u) {
+            next(2, u);
+            const uint32_t base = st0 + stage * G::bytes(seg);
+            const int s0 = u * seg, cnt = min(seg, a.S - s0);
+            auto store = [&](int s, const uint32_t (&o)[16]) {
+                if (b.want_dsrc && valid) store_bf16x32(b.dsrc[s] + n * b.dsrc_ld + c0, a.D - c0, b.wide_src, o);
+            };
+            // one row's gradient and its part of dq; RAGGED: some thread of the warp has channels outside the key
+            auto grad = [&](auto ragged_c, int r) {
+                constexpr bool RAGGED = decltype(ragged_c)::value;
+                const int s = s0 + r;
+                const f2 as = f2_dup(al[s]), x1 = f2_dup(k1[s]);
+                const CacheCodes<BITS> w = G::codes(base, code_at, r);
+                const float sc = RAGGED && !mask ? 0.0f : G::scale(base, scale_at, r);
+                const float y = valid ? k1[s] * sc : 0.0f, z = k2[s] * sc;
+                uint32_t h[16], o[16];
+                w.unpack(h);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    if (!(mask >> (2 * i) & 1u)) x[i].x = 0.0f;
-                    if (!(mask >> (2 * i + 1) & 1u)) x[i].y = 0.0f;
-                    d[i] = ffma2(q[i], make_float2(k1, k1), ffma2(x[i], make_float2(k2, k2), d[i]));
-                    if (valid) dq[i] = ffma2(x[i], make_float2(k1, k1), dq[i]);
+                    if constexpr (RAGGED)
+                        h[i] &= (mask >> (2 * i) & 1u ? 0xffffu : 0u) | (mask >> (2 * i + 1) & 1u ? 0xffff0000u : 0u);
+                    const f2 v = f2_half(h[i]);
+                    dq[i] = f2_fma(v, f2_dup(y), dq[i]);
+                    o[i] = f2_to_bf16(f2_fma(v, f2_dup(z), f2_fma(q[i], x1, f2_mul(g[i], as))));
                 }
+                store(s, o);
+            };
+            if (!warp_key) {
+                for (int r = 0; r < cnt; ++r) {
+                    const f2 as = f2_dup(al[s0 + r]);
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = f2_to_bf16(f2_mul(g[i], as));
+                    store(s0 + r, o);
+                }
+            } else if (ragged) {
+                for (int r = 0; r < cnt; ++r) grad(std::true_type{}, r);
+            } else {
+                for (int r = 0; r < cnt; ++r) grad(std::false_type{}, r);
             }
-            if (out && valid) store_bf16(out + n * ld, c0, a.D, d);
+            if (LIVE && u == nseg - 1) {
+                const float as = al[a.S], x1 = k1[a.S], y1 = valid ? x1 : 0.0f, y2 = k2[a.S];
+                uint32_t o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t u = u4_get(G::bf16_part(tok + G::BF16, i / 4), i % 4);
+                    if (!(mask >> (2 * i) & 1u)) u &= 0xffff0000u;
+                    if (!(mask >> (2 * i + 1) & 1u)) u &= 0x0000ffffu;
+                    const f2 v = f2_bf16(u);
+                    dq[i] = f2_fma(v, f2_dup(y1), dq[i]);
+                    f2 d = f2_mul(g[i], f2_dup(as));
+                    d = f2_fma(q[i], f2_dup(x1), d);
+                    o[i] = f2_to_bf16(f2_fma(v, f2_dup(y2), d));
+                }
+                if (b.dlive && valid) store_bf16x32(b.dlive + n * b.dlive_ld + c0, a.D - c0, b.wide_live, o);
+            }
+            done(2, u);
         }
-        if (MULTI) __syncthreads();
-        else __syncwarp();
+        tb ^= 1;
     }
+    cp_async_wait<0>();
     // one partial row per CTA: the teams' sums are added in team order
     const int W = a.R + (NORM ? a.D : 0);
     float* part = b.part + static_cast<size_t>(blockIdx.x) * W;
+    const int teams = MULTI ? 1 : warps * TW, team = MULTI ? 0 : wid * TW + tw;
     for (int u = 0; u < teams; ++u) {
         if (team == u && has) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float x = i & 1 ? dq[i / 2].y : dq[i / 2].x;
-                const float y = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+                const float x = i & 1 ? f2_get(dq[i / 2]).y : f2_get(dq[i / 2]).x;
                 const int j = c0 + i - a.ko;
                 if (mask >> i & 1u) part[j] = u ? part[j] + x : x;
-                if (NORM && c0 + i < a.D) part[a.R + c0 + i] = u ? part[a.R + c0 + i] + y : y;
+                if (NORM && c0 + i < a.D) {
+                    const float y = i & 1 ? f2_get(dw[i / 2]).y : f2_get(dw[i / 2]).x;
+                    part[a.R + c0 + i] = u ? part[a.R + c0 + i] + y : y;
+                }
             }
         }
         __syncthreads();
@@ -240,45 +412,47 @@ __global__ void __launch_bounds__(256) cached_bwd_kernel(const CachedBwdArgs b) 
 }
 
 template <int BITS, int LW, bool MULTI>
-cudaError_t launch_t(const CachedBwdArgs& b, int grid, cudaStream_t stream) {
-    const int block = cached_block(b.c.D), teams = MULTI ? 1 : block / LW;
-    const size_t smem = static_cast<size_t>(teams) * (b.c.S + 1) * sizeof(float);
-    auto kern = b.c.w_o ? cached_bwd_kernel<BITS, LW, MULTI, true> : cached_bwd_kernel<BITS, LW, MULTI, false>;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t launch_t(CachedBwdArgs& b, int grid, int sm_count, cudaStream_t stream) {
+    const bool live = b.c.live != nullptr, norm = b.c.w_o != nullptr;
+    const BwdPlan p = plan_t<BITS, LW, MULTI>(b.c.S, live, b.c.N, b.c.D, sm_count);
+    if (p.grid != grid) return cudaErrorInvalidConfiguration;
+    b.seg = p.seg;
+    auto kern = norm ? (live ? cached_bwd_kernel<BITS, LW, MULTI, true, true> : cached_bwd_kernel<BITS, LW, MULTI, true, false>)
+                     : (live ? cached_bwd_kernel<BITS, LW, MULTI, false, true> : cached_bwd_kernel<BITS, LW, MULTI, false, false>);
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem));
     if (err != cudaSuccess) return err;
-    return launch_pdl(kern, dim3(grid), dim3(block), smem, stream, b);
+    return launch_pdl(kern, dim3(grid), dim3(p.block), p.smem, stream, b);
 }
 
-template <int BITS>
-cudaError_t launch_bits(const CachedBwdArgs& b, int grid, cudaStream_t stream) {
-    switch (cached_team(b.c.D)) {
-        case 1: return launch_t<BITS, 1, false>(b, grid, stream);
-        case 2: return launch_t<BITS, 2, false>(b, grid, stream);
-        case 4: return launch_t<BITS, 4, false>(b, grid, stream);
-        case 8: return launch_t<BITS, 8, false>(b, grid, stream);
-        case 16: return launch_t<BITS, 16, false>(b, grid, stream);
-        case 32: return launch_t<BITS, 32, false>(b, grid, stream);
-        default: return launch_t<BITS, 32, true>(b, grid, stream);
+// f(integral constants BITS, LW, MULTI) for a row width and format
+template <int BITS, typename F>
+auto by_team(int D, F f) {
+    using B = std::integral_constant<int, BITS>;
+    switch (cached_team(D)) {
+        case 1: return f(B{}, std::integral_constant<int, 1>{}, std::false_type{});
+        case 2: return f(B{}, std::integral_constant<int, 2>{}, std::false_type{});
+        case 4: return f(B{}, std::integral_constant<int, 4>{}, std::false_type{});
+        case 8: return f(B{}, std::integral_constant<int, 8>{}, std::false_type{});
+        case 16: return f(B{}, std::integral_constant<int, 16>{}, std::false_type{});
+        case 32: return f(B{}, std::integral_constant<int, 32>{}, std::false_type{});
+        default: return f(B{}, std::integral_constant<int, 32>{}, std::true_type{});
     }
 }
 
 }  // namespace
 
-unsigned take_cached_bwd_error() {
-    unsigned v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, g_cached_bwd_error, sizeof v) != cudaSuccess) return 0xffffffffu;
-    if (v) cudaMemcpyToSymbol(g_cached_bwd_error, &zero, sizeof zero);
-    return v;
+int cached_bwd_grid(int S, bool live, long long N, int D, int bits, int sm_count) {
+    auto f = [&](auto bb, auto lw, auto multi) {
+        return plan_t<decltype(bb)::value, decltype(lw)::value, decltype(multi)::value>(S, live, N, D, sm_count).grid;
+    };
+    return bits == 8 ? by_team<8>(D, f) : by_team<4>(D, f);
 }
 
-int cached_bwd_grid(long long N, int D, int sm_count) {
-    const int block = cached_block(D), team = cached_team(D), teams = team > 32 ? 1 : block / team;
-    const long long want = (N + teams - 1) / teams, most = static_cast<long long>(sm_count) * (512 / block);
-    return static_cast<int>(want < most ? want : most);
-}
-
-cudaError_t launch_cached_bwd(const CachedBwdArgs& b, int bits, int grid, cudaStream_t stream) {
-    return bits == 8 ? launch_bits<8>(b, grid, stream) : launch_bits<4>(b, grid, stream);
+cudaError_t launch_cached_bwd(CachedBwdArgs& b, int bits, int grid, int sm_count, cudaStream_t stream) {
+    auto f = [&](auto bb, auto lw, auto multi) {
+        return launch_t<decltype(bb)::value, decltype(lw)::value, decltype(multi)::value>(b, grid, sm_count, stream);
+    };
+    return bits == 8 ? by_team<8>(b.c.D, f) : by_team<4>(b.c.D, f);
 }
 
 }  // namespace attnres

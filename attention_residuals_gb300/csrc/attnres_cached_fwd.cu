@@ -10,7 +10,7 @@
 // source, read last, gets its own.
 #include <type_traits>
 
-#include "cached.cuh"
+#include "cached_stage.cuh"
 #include "kernels.cuh"
 #include "launch_pdl.cuh"
 
@@ -43,82 +43,32 @@ __device__ __forceinline__ void load_query(const CachedArgs& a, int c0, uint32_t
     back = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const float2 f = bf2_to_f2(b[i]);
+        const float2 f = f2_get(f2_bf16(b[i]));
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(f.y * up), "f"(f.x * up));
     }
     any = c0 < a.ko + a.R && c0 + 32 > a.ko;
 }
 
-// Shared memory of one warp: kStages segments of raw rows, then the
-// segment's coefficients.  A row of a segment is the codes of the warp's 32
-// threads (16 or 32 bytes each), then the scales and the statistics of its
-// tokens.  A warp fills and reads its own part only, so the copies need no
-// barrier wider than the warp.
 constexpr int kStages = 2;
 constexpr int kSegmentBytes = 5632;  // of a warp's rows in one stage (20 warps of an SM, two stages: 220 KB)
 
-template <int BITS, int LW>
-struct Seg {
-    static constexpr int CH = BITS / 4;                           // 16-byte chunks of codes a thread
-    static constexpr int TW = 32 / LW;                            // tokens a warp
-    static constexpr int SC = LW >= 8 ? 32 : TW * 8;              // scale bytes a row
-    static constexpr int ROW = 512 * CH + SC + 8 * TW;            // bytes a row
-    static constexpr int MOST = kSegmentBytes / ROW;
-    __host__ __device__ static int rows(int S) {                  // rows a segment
+// Shared memory of a warp: two stages of a segment of rows, the segment's
+// coefficients and (unless they are the CTA's) its dots.
+template <int BITS, int LW, bool MULTI>
+struct Seg : RowStage<BITS, LW, MULTI> {
+    using R = RowStage<BITS, LW, MULTI>;
+    static constexpr int MOST = kSegmentBytes / R::ROW;
+    __host__ __device__ static int rows(int S) {  // rows a segment
         const int n = (S + MOST - 1) / MOST;
         return (S + n - 1) / n;
     }
-    __host__ __device__ static int stage(int seg) { return (seg * ROW + 15) & ~15; }
-    __host__ __device__ static int coef(int seg) { return (TW * (seg + 2) * 4 + 15) & ~15; }
-    __host__ __device__ static int warp(int seg) { return kStages * stage(seg) + 2 * coef(seg); }
+    __host__ __device__ static int coef(int seg) { return (R::TW * (seg + 2) * 4 + 15) & ~15; }
+    __host__ __device__ static int warp(int seg) { return kStages * R::bytes(seg) + 2 * coef(seg); }
 };
-
-// 16-byte asynchronous copy past L1; zeros where !on (the source is not read).
-__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int LW>
-__device__ __forceinline__ float lanes_sum(float x) {
-#pragma unroll
-    for (int o = LW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-template <int LW>
-__device__ __forceinline__ float lanes_max(float x) {
-#pragma unroll
-    for (int o = LW / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
-
-// Sums of K (1, 2 or 4) values over the LW lanes of a team, written to out[0..K).
-template <int LW, int K>
-__device__ __forceinline__ void lanes_sum_to(float (&p)[K], float* out) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (LW == 32) {  // one lane in 32 / K ends up with one of the sums
-        warp_reduce_scatter<K>(p, lane);
-        if ((lane & (32 / K - 1)) == 0) out[lane / (32 / K)] = p[0];
-    } else {
-#pragma unroll
-        for (int o = LW / 2; o > 0; o >>= 1) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) p[i] += __shfl_xor_sync(0xffffffffu, p[i], o);
-        }
-        if (lane % LW == 0) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) out[i] = p[i];
-        }
-    }
-}
 
 template <int BITS, int LW, bool MULTI, bool NORM, bool LIVE>
 __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) {
-    using G = Seg<BITS, LW>;
+    using G = Seg<BITS, LW, MULTI>;
     constexpr int CH = G::CH, TW = G::TW;
     extern __shared__ __align__(16) unsigned char dyn[];
     pdl_wait();
@@ -128,13 +78,12 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
     const int c0 = t * 32;
     const int SL = a.S + (LIVE ? 1 : 0);
     const int seg = G::rows(a.S), nseg = (a.S + seg - 1) / seg;
-    const int groups = (a.D + 31) / 32;
     unsigned char* mine = dyn + wid * G::warp(seg);
-    float* coef = reinterpret_cast<float*>(mine + kStages * G::stage(seg)) + tw * (seg + 2);
+    float* coef = reinterpret_cast<float*>(mine + kStages * G::bytes(seg)) + tw * (seg + 2);
     // dots of a segment: per warp, or for all warps of a team in two buffers used in turn
     unsigned char* rest = dyn + warps * G::warp(seg);
     float* red = MULTI ? reinterpret_cast<float*>(rest)
-                       : reinterpret_cast<float*>(mine + kStages * G::stage(seg) + G::coef(seg)) + tw * (seg + 2);
+                       : reinterpret_cast<float*>(mine + kStages * G::bytes(seg) + G::coef(seg)) + tw * (seg + 2);
     if (MULTI) rest += (2 * warps * (seg + 2) * 4 + 15) & ~15;
     float* zbuf = reinterpret_cast<float*>(rest) + (MULTI ? 0 : (wid * TW + tw) * 2 * SL);  // logits, then 1 / RMS
     const unsigned char** rows = reinterpret_cast<const unsigned char**>(
@@ -146,6 +95,7 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
     load_query(a, c0, q, back, key);
     const bool has = c0 < a.D;
     const bool warp_key = __any_sync(0xffffffffu, key);
+    const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0;
     __syncthreads();
 
     // tokens of a CTA step: one for a team of several warps, else TW a warp
@@ -156,74 +106,11 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
 
     const uint32_t st0 = smem_u32(mine);
     auto issue = [&](int stage, long long n0, int g) {
-        const uint32_t base = st0 + stage * G::stage(seg);
-        const int s0 = g * seg, cnt = min(seg, a.S - s0);
-        long long off[CH];
-        bool on[CH];
-        uint32_t dst[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = lane + 32 * i;
-            const int team = c / (LW * CH), x = (c % (LW * CH) + (MULTI ? wid * 32 * CH : 0)) * 16;
-            off[i] = min(n0 + team, a.N - 1) * a.row_ld + x;
-            on[i] = x < static_cast<int>(a.codes);
-            if (!on[i]) off[i] -= x;
-            dst[i] = base + (CH == 2 ? c ^ ((c >> 3) & 1) : c) * 16;  // keeps the 32-byte reads off each other's banks
-        }
-        for (int r = 0; r < cnt; ++r) {
-            const unsigned char* p = rows[s0 + r];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) cp_async_16z(dst[i] + r * 512 * CH, p + off[i], on[i]);
-        }
-        const uint32_t sc = base + seg * 512 * CH, stt = sc + seg * G::SC;
-        if constexpr (LW >= 16) {
-            constexpr int H = LW / 16;  // chunks of 16 scales a token
-            for (int i = lane; i < cnt * TW * H; i += 32) {
-                const int r = i / (TW * H), team = i / H % TW, h = i % H;
-                const int x = (MULTI ? wid * 32 : 0) + h * 16;
-                if (x < groups)
-                    cp_async_16z(sc + r * 32 + team * LW + h * 16,
-                                 rows[s0 + r] + min(n0 + team, a.N - 1) * a.row_ld + a.codes + x, true);
-            }
-        } else {
-            for (int i = lane; i < cnt * TW; i += 32) {
-                const int r = i / TW, team = i % TW;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sc + r * G::SC + team * 8),
-                             "l"(rows[s0 + r] + min(n0 + team, a.N - 1) * a.row_ld + a.codes)
-                             : "memory");
-            }
-        }
-        for (int i = lane; i < cnt * TW; i += 32) {
-            const int r = i / TW, team = i % TW;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(stt + i * 8),
-                         "l"(rows[s0 + r] + min(n0 + team, a.N - 1) * a.row_ld + a.stat)
-                         : "memory");
-        }
+        G::copy(a, rows, st0 + stage * G::bytes(seg), seg, n0, g * seg, min(seg, a.S - g * seg));
         cp_async_commit();
     };
-    // this thread's codes and scale byte of a segment's row 0
-    uint32_t code_at[CH];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = lane * CH + i;
-        code_at[i] = (CH == 2 ? c ^ ((c >> 3) & 1) : c) * 16;
-    }
-    const uint32_t scale_at = seg * 512 * CH + (LW >= 8 ? lane : tw * 8 + l);
-    auto codes = [&](uint32_t base, int r) {
-        CacheCodes<BITS> w;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const uint4 u = lds128(base + code_at[i] + r * 512 * CH);
-            w.w[4 * i] = u.x, w.w[4 * i + 1] = u.y, w.w[4 * i + 2] = u.z, w.w[4 * i + 3] = u.w;
-        }
-        return w;
-    };
-    // a thread without channels reads some other byte: its codes are zero and its sums unused
-    auto scale_of = [&](uint32_t base, int r) {
-        uint32_t b;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(base + scale_at + r * G::SC));
-        return cache_scale(b);
-    };
+    uint32_t code_at[CH], scale_at;
+    G::places(seg, code_at, scale_at);
     // dots of rows r0 .. r0 + K - 1 with the query, summed over the team's lanes of this warp
     auto dots = [&](auto count, uint32_t base, int r0, float* out) {
         constexpr int K = decltype(count)::value;
@@ -231,7 +118,7 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
         CacheCodes<BITS> w[K];
         float sc[K];
 #pragma unroll
-        for (int r = 0; r < K; ++r) w[r] = codes(base, r0 + r), sc[r] = scale_of(base, r0 + r);
+        for (int r = 0; r < K; ++r) w[r] = G::codes(base, code_at, r0 + r), sc[r] = G::scale(base, scale_at, r0 + r);
 #pragma unroll
         for (int r = 0; r < K; ++r) {
             uint32_t h[16];
@@ -259,9 +146,9 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
             for (int i = 0; i < 4; ++i)
                 lv[i] = c0 + 8 * i < a.D ? ld_global_nc_v4(x + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
         }
-        float2 acc[16];
+        f2 acc[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < 16; ++i) acc[i] = 0ull;
         float mx = __uint_as_float(0xff800000u), sum = 0.0f;
         for (int g = 0; g < nseg; ++g) {
             // the next segment (of this token or the next one) is copied while this one is read
@@ -273,7 +160,7 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
                 cp_async_wait<0>();
             }
             __syncwarp();
-            const uint32_t base = st0 + stage * G::stage(seg);
+            const uint32_t base = st0 + stage * G::bytes(seg);
             const int s0 = g * seg, cnt = min(seg, a.S - s0);
             const bool with_live = LIVE && last;
             float* out = MULTI ? red + (flip * warps + wid) * (seg + 2) : red;
@@ -321,8 +208,7 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
                 if (with_live && s == cnt) {
                     rs = rsqrtf(ms / static_cast<float>(a.R) + a.eps);
                 } else {
-                    const uint2 stv = *reinterpret_cast<const uint2*>(mine + stage * G::stage(seg) +
-                                                                      seg * (512 * CH + G::SC) + (s * TW + tw) * 8);
+                    const uint2 stv = G::stat(base, seg, s, tw);
                     rs = rsqrtf(__uint_as_float(stv.x) + a.eps);
                     if (stv.y != a.tag) {
                         if (valid) atomicCAS(&g_cached_fwd_error, 0u, static_cast<unsigned>(kSiteCacheTag));
@@ -347,20 +233,20 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
             __syncwarp();
             if (g > 0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = fmul2(acc[i], make_float2(corr, corr));
+                for (int i = 0; i < 16; ++i) acc[i] = f2_mul(acc[i], f2_dup(corr));
             }
             auto mix = [&](auto count, int r0) {
                 constexpr int K = decltype(count)::value;
                 CacheCodes<BITS> w[K];
                 float c[K];
 #pragma unroll
-                for (int r = 0; r < K; ++r) w[r] = codes(base, r0 + r), c[r] = coef[r0 + r] * scale_of(base, r0 + r);
+                for (int r = 0; r < K; ++r) w[r] = G::codes(base, code_at, r0 + r), c[r] = coef[r0 + r] * G::scale(base, scale_at, r0 + r);
 #pragma unroll
                 for (int r = 0; r < K; ++r) {
                     uint32_t h[16];
                     w[r].unpack(h);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[i] = ffma2(half2_to_f2(h[i]), make_float2(c[r], c[r]), acc[i]);
+                    for (int i = 0; i < 16; ++i) acc[i] = f2_fma(f2_half(h[i]), f2_dup(c[r]), acc[i]);
                 }
             };
             {
@@ -372,19 +258,19 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
             if (with_live) {
                 const float c = coef[cnt];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = ffma2(bf2_to_f2(u4_get(lv[i / 4], i % 4)), make_float2(c, c), acc[i]);
+                for (int i = 0; i < 16; ++i) acc[i] = f2_fma(f2_bf16(u4_get(lv[i / 4], i % 4)), f2_dup(c), acc[i]);
             }
             __syncwarp();  // the stage and the coefficients are free again
             stage ^= 1;
             flip ^= 1;
         }
         const float inv = 1.0f / sum;
-        float2 out2 = make_float2(inv, inv);
+        f2 out2 = f2_dup(inv);
         if constexpr (NORM) {
-            float2 ss = make_float2(0.0f, 0.0f);
+            f2 ss = 0ull;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ss = ffma2(acc[i], acc[i], ss);
-            float s1 = lanes_sum<LW>(has ? ss.x + ss.y : 0.0f);
+            for (int i = 0; i < 16; ++i) ss = f2_fma(acc[i], acc[i], ss);
+            float s1 = lanes_sum<LW>(has ? f2_sum(ss) : 0.0f);
             if constexpr (MULTI) {
                 float* out = red + flip * warps * (seg + 2);
                 if (lane == 0) out[wid] = s1;
@@ -395,27 +281,24 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
             }
             const float o_rstd = rsqrtf(s1 * inv * inv / static_cast<float>(a.D) + a.eps);
             if (t == 0 && valid) a.o_rstd[n] = o_rstd;
-            out2 = make_float2(inv * o_rstd, inv * o_rstd);
+            out2 = f2_dup(inv * o_rstd);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (NORM) {
                 const uint4 w = c0 + 8 * i < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + c0) + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[4 * i + k] = fmul2(fmul2(acc[4 * i + k], out2), bf2_to_f2(u4_get(w, k)));
+                for (int k = 0; k < 4; ++k) acc[4 * i + k] = f2_mul(f2_mul(acc[4 * i + k], out2), f2_bf16(u4_get(w, k)));
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[4 * i + k] = fmul2(acc[4 * i + k], out2);
+                for (int k = 0; k < 4; ++k) acc[4 * i + k] = f2_mul(acc[4 * i + k], out2);
             }
         }
         if (valid) {
-            uint16_t* y = a.y + n * a.D + c0;
+            uint32_t o[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (c0 + 8 * i < a.D)
-                    *reinterpret_cast<uint4*>(y + 8 * i) = make_uint4(pack_f2(acc[4 * i]), pack_f2(acc[4 * i + 1]),
-                                                                      pack_f2(acc[4 * i + 2]), pack_f2(acc[4 * i + 3]));
-            }
+            for (int i = 0; i < 16; ++i) o[i] = f2_to_bf16(acc[i]);
+            store_bf16x32(a.y + n * a.D + c0, a.D - c0, wide, o);
             if (!MULTI || wid == 0) {
                 for (int s = l; s < SL; s += LW) {
                     const float z = zbuf[s];
@@ -431,7 +314,7 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
 
 template <int BITS, int LW, bool MULTI>
 cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
-    using G = Seg<BITS, LW>;
+    using G = Seg<BITS, LW, MULTI>;
     const int block = cached_block(a.D), warps = block / 32, SL = a.S + (a.live ? 1 : 0);
     const int seg = G::rows(a.S), per = MULTI ? 1 : warps * G::TW;
     size_t smem = static_cast<size_t>(warps) * G::warp(seg);

@@ -60,14 +60,46 @@ __device__ __forceinline__ void cache_unpack4(uint32_t w, uint32_t& a, uint32_t&
         : "r"(w));
 }
 
-// Half pair -> two floats.
-__device__ __forceinline__ float2 half2_to_f2(uint32_t h) {
+// A pair of floats as one 64-bit register, so that it stays an aligned pair
+// from one packed instruction to the next.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ f2 f2_dup(float x) { return f2_make(x, x); }
+__device__ __forceinline__ float2 f2_get(f2 v) {
     float2 r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    const float2 r = f2_get(v);
+    return r.x + r.y;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_half(uint32_t h) {  // of a half pair, as half * 1 + 0
+    f2 r;
+    asm("{\n\t.reg .b16 l, h, one;\n\t.reg .f32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b16 one, 0x3c00;\n\t"
+        "fma.rn.f32.f16 x, l, one, 0f00000000;\n\tfma.rn.f32.f16 y, h, one, 0f00000000;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
         : "r"(h));
     return r;
 }
+__device__ __forceinline__ f2 f2_bf16(uint32_t w) {  // of a bf16 pair
+    return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t f2_to_bf16(f2 v) { return pack_f2(f2_get(v)); }
 
 // s0 += a_lo * b_lo, s1 += a_hi * b_hi for half pairs (exact products, FP32 sums).
 __device__ __forceinline__ void half2_dot(uint32_t a, uint32_t b, float& s0, float& s1) {
@@ -125,6 +157,8 @@ struct CachedBwdArgs {
     uint16_t* dsrc[ATTNRES_MAX_S];
     long long dsrc_ld, dlive_ld;
     int want_dsrc;
+    int wide_src, wide_live;  // gradient rows start on 32-byte boundaries and D % 16 == 0
+    int seg;                  // rows a segment (the launcher's)
     uint16_t* dlive;
     const uint16_t* dy;
     float* part;  // [grid][R + D with the output norm]
@@ -147,10 +181,9 @@ inline int cached_block(int D) {
 cudaError_t launch_cache_write(const CacheRowsArgs& a, int bits, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_load(const CacheRowsArgs& a, int bits, int sm_count, cudaStream_t stream);
 cudaError_t launch_cached_fwd(const CachedArgs& a, int bits, int sm_count, cudaStream_t stream);
-int cached_bwd_grid(long long N, int D, int sm_count);
-cudaError_t launch_cached_bwd(const CachedBwdArgs& a, int bits, int grid, cudaStream_t stream);
+int cached_bwd_grid(int S, bool live, long long N, int D, int bits, int sm_count);
+cudaError_t launch_cached_bwd(CachedBwdArgs& a, int bits, int grid, int sm_count, cudaStream_t stream);
 unsigned take_cache_rows_error();
 unsigned take_cached_fwd_error();
-unsigned take_cached_bwd_error();
 
 }  // namespace attnres
