@@ -10,8 +10,8 @@ marshalled here and CPU tensors are rejected.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+from functools import lru_cache
 from typing import Optional, Sequence, Union
 
 import torch
@@ -22,6 +22,7 @@ from .ops import EPS_DEFAULT, _as_rows, _check_out, _check_vec, _out_rows
 Records = Union[torch.Tensor, Sequence[torch.Tensor]]
 
 
+@lru_cache(maxsize=None)
 def attnres_cache_row_bytes(D: int, bits: int) -> int:
     """Bytes of one token's record (a multiple of 16)."""
     n = int(_lib.load().attnres_cache_row_bytes(int(D), int(bits)))
@@ -30,15 +31,22 @@ def attnres_cache_row_bytes(D: int, bits: int) -> int:
     return n
 
 
-def _on(device):
-    """The tensors' device made current, if it is not."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _stream_of(stream, device) -> int:
+def _call(name: str, device, stream, *args) -> None:
+    """The library's function `name` with `args` and the stream (by default the
+    current one of the tensors' device), that device current."""
+    f = getattr(_lib.load(), name)
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream)
+    if rc:
+        _lib.check(rc, name)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -52,35 +60,42 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
 
 
 def _bf16_rows(t: torch.Tensor, name: str):
-    """[N, D] view of bf16 rows and their stride (a copy where the rows cannot be addressed)."""
+    """(address, tokens, elements between rows, what keeps the rows alive); a
+    copy is made where the rows cannot be addressed."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bf16 tensor")
-    r = _as_rows(t, t.shape[-1])
-    ld = r.stride(0) if r.shape[0] > 1 else r.shape[1]
+    D = t.shape[-1]
+    if t.is_contiguous():
+        r, n, ld = t, t.numel() // D if D else 0, D
+    else:
+        r = _as_rows(t, D)
+        n, ld = r.shape[0], r.stride(0) if r.shape[0] > 1 else D
     if r.data_ptr() % 16 or ld % 8:
-        r = _aligned(r)
-        ld = r.shape[1]
-    return r, ld
+        r, ld = _aligned(r), D
+    return r.data_ptr(), n, ld, r
 
 
 def _record_rows(t: torch.Tensor, size: int, writable: bool = False):
-    """[N, size] view of records and the bytes between them."""
+    """(address, tokens, bytes between records, what keeps them alive)."""
     if t.dtype != torch.uint8 or not t.is_cuda:
         raise TypeError("records must be CUDA uint8 tensors")
     if t.dim() < 1 or t.shape[-1] != size:
         raise ValueError(f"records must be [..., {size}] for this D and bits")
+    n = t.numel() // size
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t.data_ptr(), n, size, t
     try:
-        r = t.view(-1, size) if t.numel() else t.reshape(0, size)
+        r = t.view(-1, size) if n else t.reshape(0, size)
     except RuntimeError as e:
         if writable:
             raise ValueError("out: records must be addressable as [N, bytes]") from e
         r = t.contiguous().view(-1, size)
-    ld = r.stride(0) if r.shape[0] > 1 else size
-    if (size and r.numel() and r.stride(1) != 1) or r.data_ptr() % 16 or ld % 16 or ld < size:
+    ld = r.stride(0) if n > 1 else size
+    if (n and r.stride(1) != 1) or r.data_ptr() % 16 or ld % 16 or ld < size:
         if writable:
             raise ValueError("out: records must be dense, 16-byte aligned and not overlap")
         r, ld = _aligned(r), size
-    return r, ld
+    return r.data_ptr(), n, ld, r
 
 
 class _Sources:
@@ -92,17 +107,21 @@ class _Sources:
         if isinstance(rows, torch.Tensor):
             if rows.dim() < 2 or rows.shape[0] < 1:
                 raise ValueError("packed records must be [S, ..., bytes] with S >= 1")
-            self.packed, self.lead = True, rows.shape[1:-1]
-            first, self.ld = _record_rows(rows[0], size)
-            self.N, self.device = first.shape[0], rows.device
-            if first.data_ptr() == rows.data_ptr() and rows.stride(0) % 16 == 0:
-                base, step = rows.data_ptr(), rows.stride(0)
-                self.addrs, self.keep = [base + s * step for s in range(rows.shape[0])], rows
+            S = rows.shape[0]
+            self.packed, self.lead, self.device = True, rows.shape[1:-1], rows.device
+            if rows.is_contiguous() and rows.data_ptr() % 16 == 0:
+                base, total, self.ld, self.keep = _record_rows(rows, size)
+                self.N = total // S
+                step = self.N * size
             else:
-                self.keep = rows.contiguous() if rows.data_ptr() % 16 == 0 else rows.clone(memory_format=torch.contiguous_format)
-                self.ld = size
-                base, step = self.keep.data_ptr(), self.keep.stride(0)
-                self.addrs = [base + s * step for s in range(rows.shape[0])]
+                base, self.N, self.ld, self.keep = _record_rows(rows[0], size)
+                step = rows.stride(0)
+                if base != rows.data_ptr() or step % 16:   # the first source could not be addressed in place
+                    self.keep = _aligned(rows)
+                    base, self.ld, step = self.keep.data_ptr(), size, self.N * size
+                else:
+                    self.keep = rows
+            self.addrs = [base + s * step for s in range(S)]
             return
         rows = list(rows)
         if not rows:
@@ -113,13 +132,11 @@ class _Sources:
                 raise ValueError("all sources must have the same shape")
             if r.device != self.device:
                 raise ValueError("all sources must be on one device")
-        views = [_record_rows(r, size) for r in rows]
-        lds = {ld for _, ld in views}
-        if len(lds) > 1:
-            views = [(_aligned(r), size) for r, _ in views]
-            lds = {size}
-        self.keep, self.ld, self.N = [r for r, _ in views], lds.pop(), views[0][0].shape[0]
-        self.addrs = [r.data_ptr() for r in self.keep]
+        found = [_record_rows(r, size) for r in rows]
+        if len({ld for _, _, ld, _ in found}) > 1:
+            found = [_record_rows(_aligned(r), size) for r in rows]
+        self.addrs, self.keep = [f[0] for f in found], [f[3] for f in found]
+        self.N, self.ld = found[0][1], found[0][2]
 
 
 def _params(src: _Sources, R: int, D: int, bits: int, live, key_offset, eps, scale, out_norm: bool):
@@ -138,8 +155,7 @@ def _params(src: _Sources, R: int, D: int, bits: int, live, key_offset, eps, sca
             raise ValueError("live must have the cached sources' leading shape and D channels")
         if live.device != src.device:
             raise ValueError("live must be on the records' device")
-        keep, p.live_ld = _bf16_rows(live, "live")
-        p.live = keep.data_ptr()
+        p.live, _, p.live_ld, keep = _bf16_rows(live, "live")
     return p, keep
 
 
@@ -161,22 +177,19 @@ def attnres_cache_write(values: torch.Tensor, *, bits: int = 8, key_rank: Option
         D = values.shape[-1]
         R = D if key_rank is None else key_rank
         return cache_write(values, bits, R, D - R if key_offset is None else key_offset)
-    x, ld = _bf16_rows(values, "values")
-    D = x.shape[1]
+    x, N, ld, keep = _bf16_rows(values, "values")
+    D, dev = values.shape[-1], values.device
     size = attnres_cache_row_bytes(D, bits)
     R = D if key_rank is None else int(key_rank)
-    lead = values.shape[:-1]
+    shape = (*values.shape[:-1], size)
     if out is None:
-        out = torch.empty((*lead, size), dtype=torch.uint8, device=x.device)
-    elif out.shape != (*lead, size):
-        raise ValueError(f"out must be uint8 {[*lead, size]}")
-    rows, row_ld = _record_rows(out, size, writable=True)
-    _same_device(x.device, out=out)
-    with _on(x.device):
-        rc = _lib.load().attnres_cache_write(x.data_ptr(), ld, x.shape[0], D, int(bits), R,
-                                             D - R if key_offset is None else int(key_offset), rows.data_ptr(), row_ld,
-                                             _stream_of(stream, x.device))
-    _lib.check(rc, "attnres_cache_write")
+        out = torch.empty(shape, dtype=torch.uint8, device=dev)
+    elif out.shape != shape:
+        raise ValueError(f"out must be uint8 {list(shape)}")
+    _same_device(dev, out=out)
+    rows, _, row_ld, _ = _record_rows(out, size, writable=True)
+    _call("attnres_cache_write", dev, stream, x, ld, N, D, int(bits), R,
+          D - R if key_offset is None else int(key_offset), rows, row_ld)
     torch.autograd.graph.increment_version(out)
     return out
 
@@ -188,23 +201,20 @@ def attnres_cache_load(rows: torch.Tensor, D: int, *, bits: int = 8, out: Option
         from .custom_ops import cache_load
         return cache_load(rows, D, bits)
     size = attnres_cache_row_bytes(D, bits)
-    lead = rows.shape[:-1]
-    r, row_ld = _record_rows(rows, size)
-    N = r.shape[0]
+    src, N, row_ld, keep = _record_rows(rows, size)
+    shape, dev = (*rows.shape[:-1], D), rows.device
     if out is None:
-        out = torch.empty((*lead, D), dtype=torch.bfloat16, device=rows.device)
-        dst = out.view(N, D)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        dst, ld = out.data_ptr(), D
     else:
-        if out.shape != (*lead, D):
-            raise ValueError(f"out must be bf16 {[*lead, D]}")
-        _same_device(rows.device, out=out)
-        dst = _out_rows(out, N, D, "out")
-        if dst.data_ptr() % 16 or (N > 1 and (dst.stride(0) % 8 or dst.stride(0) < D)):
+        if out.shape != shape:
+            raise ValueError(f"out must be bf16 {list(shape)}")
+        _same_device(dev, out=out)
+        r = _out_rows(out, N, D, "out")
+        dst, ld = r.data_ptr(), r.stride(0) if N > 1 else D
+        if dst % 16 or ld % 8 or ld < D:
             raise ValueError("out: rows must start on 16-byte boundaries and not overlap")
-    with _on(rows.device):
-        rc = _lib.load().attnres_cache_load(r.data_ptr(), row_ld, N, D, int(bits), dst.data_ptr(),
-                                            dst.stride(0) if N > 1 else D, _stream_of(stream, rows.device))
-    _lib.check(rc, "attnres_cache_load")
+    _call("attnres_cache_load", dev, stream, src, row_ld, N, D, int(bits), dst, ld)
     return out
 
 
@@ -222,33 +232,34 @@ def attnres_cached_fwd(rows: Records, q: torch.Tensor, D: int, *, bits: int = 8,
     w_o = None if w_o is None else _aligned(_check_vec(w_o, D, "w_o"))
     _same_device(dev, q=q, w_o=w_o)
     p, keep = _params(src, R, D, int(bits), live, key_offset, eps, scale, w_o is not None)
-    o = out or {}
-    y = o.get("y")
-    if y is None:
-        y = torch.empty((N, D), dtype=torch.bfloat16, device=dev)
-    if all(o.get(k) is None for k in ("alpha", "rstd", "logit")):
-        alpha, rstd, logit = torch.empty((3, N, S), dtype=torch.float32, device=dev).unbind(0)
-    else:
-        alpha, rstd, logit = (o[k] if o.get(k) is not None else torch.empty((N, S), dtype=torch.float32, device=dev)
-                              for k in ("alpha", "rstd", "logit"))
+    f32 = torch.float32
     o_rstd = None
-    if w_o is not None:
-        o_rstd = o.get("o_rstd")
-        if o_rstd is None:
-            o_rstd = torch.empty((N,), dtype=torch.float32, device=dev)
-    if o:
+    if out:
+        y, alpha, rstd, logit = (out.get(k) for k in ("y", "alpha", "rstd", "logit"))
         _check_out(y, N * D, torch.bfloat16, "y", dev)
-        for name, t in (("alpha", alpha), ("rstd", rstd), ("logit", logit)):
-            _check_out(t, N * S, torch.float32, name, dev)
-        _check_out(o_rstd, N, torch.float32, "o_rstd", dev)
-    with _on(dev):
-        rc = _lib.load().attnres_cached_fwd(ctypes.byref(p), _addr(q), _addr(w_o), _addr(y), _addr(alpha), _addr(rstd),
-                                            _addr(logit), _addr(o_rstd), _stream_of(stream, dev))
-    _lib.check(rc, "attnres_cached_fwd")
-    return {"y": y.view(*src.lead, D), "alpha": alpha, "rstd": rstd, "logit": logit, "o_rstd": o_rstd}
+        for name in ("alpha", "rstd", "logit"):
+            _check_out(out.get(name), N * S, f32, name, dev)
+        if w_o is not None:
+            o_rstd = out.get("o_rstd")
+            _check_out(o_rstd, N, f32, "o_rstd", dev)
+    else:
+        y = alpha = rstd = logit = None
+    shape = (*src.lead, D)
+    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if y is None else y.view(shape)
+    alpha = torch.empty((N, S), dtype=f32, device=dev) if alpha is None else alpha
+    rstd = torch.empty((N, S), dtype=f32, device=dev) if rstd is None else rstd
+    logit = torch.empty((N, S), dtype=f32, device=dev) if logit is None else logit
+    if w_o is not None and o_rstd is None:
+        o_rstd = torch.empty((N,), dtype=f32, device=dev)
+    _call("attnres_cached_fwd", dev, stream, ctypes.byref(p), q.data_ptr(), _addr(w_o), y.data_ptr(), alpha.data_ptr(),
+          rstd.data_ptr(), logit.data_ptr(), _addr(o_rstd))
+    return {"y": y, "alpha": alpha, "rstd": rstd, "logit": logit, "o_rstd": o_rstd}
 
 
-def attnres_cached_bwd_workspace_bytes(params: _lib.AttnresCachedParams) -> int:
+def _workspace_bytes(params: _lib.AttnresCachedParams, device) -> int:
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return int(_lib.load().attnres_cached_bwd_workspace_bytes(ctypes.byref(params)))
     return int(_lib.load().attnres_cached_bwd_workspace_bytes(ctypes.byref(params)))
 
 
@@ -286,8 +297,8 @@ def attnres_cached_bwd(rows: Records, q: torch.Tensor, dy: torch.Tensor, saved: 
         if dvalues is None:
             if src.packed:
                 dvalues = torch.empty((S, *shape), dtype=torch.bfloat16, device=dev)
-                base = dvalues.data_ptr()
-                addrs = [base + s * N * D * 2 for s in range(S)]
+                base, step = dvalues.data_ptr(), N * D * 2
+                addrs = [base + s * step for s in range(S)]
             else:
                 dvalues = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(S)]
                 addrs = [d.data_ptr() for d in dvalues]
@@ -310,16 +321,13 @@ def attnres_cached_bwd(rows: Records, q: torch.Tensor, dy: torch.Tensor, saved: 
     if w_o is not None:
         dw = torch.empty((D,), dtype=torch.bfloat16, device=dev)
         dw32 = torch.empty((D,), dtype=torch.float32, device=dev)
-    with _on(dev):
-        need = attnres_cached_bwd_workspace_bytes(p)
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-        rc = _lib.load().attnres_cached_bwd(
-            ctypes.byref(p), _addr(q), _addr(w_o), _addr(dy), _addr(saved["alpha"]), _addr(saved["rstd"]),
-            _addr(saved["logit"]), _addr(saved.get("o_rstd")), dptrs, dld, _addr(d_live), D, _addr(dq), _addr(dq32),
-            _addr(dw), _addr(dw32), _addr(workspace), workspace.numel() * workspace.element_size(),
-            _stream_of(stream, dev))
-    _lib.check(rc, "attnres_cached_bwd")
+    need = _workspace_bytes(p, dev)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    _call("attnres_cached_bwd", dev, stream, ctypes.byref(p), q.data_ptr(), _addr(w_o), dy.data_ptr(),
+          saved["alpha"].data_ptr(), saved["rstd"].data_ptr(), saved["logit"].data_ptr(), _addr(saved.get("o_rstd")),
+          dptrs, dld, _addr(d_live), D, dq.data_ptr(), dq32.data_ptr(), _addr(dw), _addr(dw32), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return {"dvalues": dvalues, "d_live": d_live, "dq": dq, "dq_f32": dq32, "dw_o": dw, "dw_o_f32": dw32}
 
 

@@ -417,11 +417,15 @@ cudaError_t launch_t(CachedBwdArgs& b, int grid, int sm_count, cudaStream_t stre
     const BwdPlan p = plan_t<BITS, LW, MULTI>(b.c.S, live, b.c.N, b.c.D, sm_count);
     if (p.grid != grid) return cudaErrorInvalidConfiguration;
     b.seg = p.seg;
-    auto kern = norm ? (live ? cached_bwd_kernel<BITS, LW, MULTI, true, true> : cached_bwd_kernel<BITS, LW, MULTI, true, false>)
-                     : (live ? cached_bwd_kernel<BITS, LW, MULTI, false, true> : cached_bwd_kernel<BITS, LW, MULTI, false, false>);
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem));
-    if (err != cudaSuccess) return err;
-    return launch_pdl(kern, dim3(grid), dim3(p.block), p.smem, stream, b);
+    auto run = [&](auto with_norm, auto with_live) {
+        constexpr auto kern = cached_bwd_kernel<BITS, LW, MULTI, decltype(with_norm)::value, decltype(with_live)::value>;
+        int fit = 0;
+        const cudaError_t err = kernel_fit<kern>(p.block, p.smem, &fit);
+        return err != cudaSuccess ? err : launch_pdl(kern, dim3(grid), dim3(p.block), p.smem, stream, b);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    return norm ? (live ? run(Yes{}, Yes{}) : run(Yes{}, No{})) : (live ? run(No{}, Yes{}) : run(No{}, No{}));
 }
 
 // f(integral constants BITS, LW, MULTI) for a row width and format

@@ -321,16 +321,17 @@ cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
     if (MULTI) smem += (2 * warps * (seg + 2) * 4 + 15) & ~15;
     smem += (static_cast<size_t>(per) * 2 * SL * 4 + 15) & ~size_t(15);
     smem += static_cast<size_t>(a.S) * 8;
-    auto kern = a.w_o ? (a.live ? cached_fwd_kernel<BITS, LW, MULTI, true, true> : cached_fwd_kernel<BITS, LW, MULTI, true, false>)
-                      : (a.live ? cached_fwd_kernel<BITS, LW, MULTI, false, true> : cached_fwd_kernel<BITS, LW, MULTI, false, false>);
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    int fit = 0;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, block, smem);
-    if (err != cudaSuccess) return err;
-    if (fit < 1) return cudaErrorInvalidConfiguration;
-    const long long want = (a.N + per - 1) / per, most = static_cast<long long>(sm_count) * fit;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(block), smem, stream, a);
+    auto run = [&](auto norm, auto live) {
+        constexpr auto kern = cached_fwd_kernel<BITS, LW, MULTI, decltype(norm)::value, decltype(live)::value>;
+        int fit = 0;
+        const cudaError_t err = kernel_fit<kern>(block, smem, &fit);
+        if (err != cudaSuccess) return err;
+        const long long want = (a.N + per - 1) / per, most = static_cast<long long>(sm_count) * fit;
+        return launch_pdl(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(block), smem, stream, a);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    return a.w_o ? (a.live ? run(Yes{}, Yes{}) : run(Yes{}, No{})) : (a.live ? run(No{}, Yes{}) : run(No{}, No{}));
 }
 
 template <int BITS>

@@ -16,6 +16,8 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
+
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -176,6 +178,38 @@ inline int cached_team(int D) {
 inline int cached_block(int D) {
     const int t = cached_team(D);
     return t > 32 ? t : 128;
+}
+
+// Raises a kernel's dynamic shared memory limit to `smem`, once a device and
+// size, and says how many of its CTAs share an SM (registers and memory).
+template <auto Kernel>
+inline cudaError_t kernel_fit(int block, size_t smem, int* fit) {
+    struct Known {
+        size_t limit;
+        int block, fit;
+        size_t smem;
+    };
+    static std::mutex lock;
+    static Known known[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    std::lock_guard<std::mutex> hold(lock);
+    Known local{};
+    Known& k = dev < 64 ? known[dev] : local;
+    if (smem > k.limit) {
+        err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+        k.limit = smem;
+    }
+    if (k.block != block || k.smem != smem) {
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k.fit, Kernel, block, smem);
+        if (err != cudaSuccess) return err;
+        k.block = block;
+        k.smem = smem;
+    }
+    *fit = k.fit;
+    return k.fit > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 cudaError_t launch_cache_write(const CacheRowsArgs& a, int bits, int sm_count, cudaStream_t stream);
