@@ -312,6 +312,10 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
     }
 }
 
+// Tokens from which rows of more than 512 channels go to the kernel with a
+// warp or two a token; fewer are finished sooner by more threads each.
+constexpr long long kWideTokens = 1;
+
 template <int BITS, int LW, bool MULTI>
 cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
     using G = Seg<BITS, LW, MULTI>;
@@ -357,6 +361,8 @@ unsigned take_cached_fwd_error() {
 }
 
 cudaError_t launch_cached_fwd(const CachedArgs& a, int bits, int sm_count, cudaStream_t stream) {
+    if (cached_team(a.D) >= 32 && a.N >= kWideTokens)
+        return bits == 8 ? launch_cached_wide8(a, sm_count, stream) : launch_cached_wide4(a, sm_count, stream);
     return bits == 8 ? launch_bits<8>(a, sm_count, stream) : launch_bits<4>(a, sm_count, stream);
 }
 

@@ -1,0 +1,526 @@
+// attnres_cached_wide.cuh -- the softmax read over many tokens of compressed
+// rows of more than 512 channels: one warp a token (two above 4096 channels).
+//
+// A lane owns up to four groups of 32 channels and keeps their FP32 mixture in
+// registers, so what a token costs besides its values (the sums over the warp,
+// the softmax, addresses) is paid once for up to 4096 channels, and warps wait
+// for nobody.  Segments of records come to the warp's own shared memory by
+// bulk copies, one a record; per segment
+//   1. dots with the query, halves by halves with FP32 sums (fma.rn.f32.f16),
+//      a block of rows at a time, so that the query is read once a block
+//   2. the running softmax, a lane a row
+//   3. mixture: codes decoded again, widened and added in FP32; a slot that
+//      has been read takes the next segment's record at once.
+// What bounds it: instruction issue.  Decoding costs half an instruction a
+// value, the dot one, widening one, the packed FMA a half.
+#pragma once
+
+#include <type_traits>
+
+#include "cached_stage.cuh"
+#include "kernels.cuh"
+#include "launch_pdl.cuh"
+
+namespace attnres {
+namespace {
+
+__device__ unsigned g_cached_wide_error;
+
+// Warps of the one CTA an SM runs, by groups a lane: a multiple of the four
+// schedulers whose registers hold the mixture (32 a group) without spilling.
+__host__ __device__ constexpr int wide_warps(int nc) { return nc == 4 ? 8 : nc == 1 ? 20 : 12; }
+constexpr int kWideSmem = 227 * 1024;
+
+struct WidePlan {
+    int seg;                  // records a segment, and slots a warp
+    uint32_t slot;            // bytes of a slot: the warp's part of a record
+    uint32_t codes, scales;   // of a slot: bytes of codes, where the scales begin
+    uint32_t stat;            // where the statistic is in a slot
+    uint32_t q_at, back_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
+    uint32_t red_at, coef_at, z_at, bar_at;                         // in a warp's
+    size_t smem;
+};
+
+WidePlan wide_plan(int D, int S, bool live, int bits, int nc, int w) {
+    WidePlan p{};
+    const uint32_t rec = cache_row_bytes(D, bits), codes = cache_code_bytes(D, bits), stat = cache_stat_offset(D, bits);
+    const int SL = S + (live ? 1 : 0), warps = wide_warps(nc);
+    if (w == 1) {
+        p.slot = rec;
+        p.codes = p.scales = codes;
+        p.stat = stat;
+    } else {  // the warp's codes, its scales, and the 16 bytes that hold the statistic
+        p.codes = p.scales = static_cast<uint32_t>(nc) * 32 * 4 * bits;
+        p.slot = p.codes + nc * 32 + 16;
+        p.stat = p.codes + nc * 32 + stat % 16;
+    }
+    uint32_t off = 0;
+    auto take = [&](uint32_t bytes) {
+        const uint32_t at = off;
+        off += (bytes + 15u) & ~15u;
+        return at;
+    };
+    p.q_at = take(nc * w * 32 * 64);
+    p.back_at = take(nc * w * 32 * 4);
+    p.rows_at = take(S * 8);
+    p.abort_at = take(16);
+    p.warp_at = off;
+    off = 0;
+    p.bar_at = take(16);
+    p.z_at = take(2 * SL * 4);
+    p.red_at = take(2 * 32 * 4);
+    p.coef_at = take(32 * 4);
+    const uint32_t room = (kWideSmem - p.warp_at) / warps - off - 16;
+    int most = static_cast<int>(room / p.slot);
+    if (most > 30) most = 30;
+    if (most < 1) most = 1;
+    const int n = (S + most - 1) / most;
+    p.seg = (S + n - 1) / n;
+    p.warp_bytes = off + ((p.seg * p.slot + 15) & ~15u);
+    p.smem = p.warp_at + static_cast<size_t>(warps) * p.warp_bytes;
+    return p;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// All lanes meet here, each after `v`, which must be computed from the last
+// shared-memory loads of what is then overwritten by a bulk copy: the vote
+// cannot issue while a load is in flight.
+__device__ __forceinline__ void read_done(f2 v) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.eq.u64 p, %0, 0x7fc12345;\n\tvote.sync.any.pred q, p, 0xffffffff;\n\t}" ::"l"(v) : "memory");
+    __syncwarp();
+}
+
+// The query's channels of one group as halves, scaled by a power of two that
+// puts the largest magnitude in [2^14, 2^15) (`back` undoes it).  bf16 has
+// fewer significand bits than a half, so every channel down to 2^-28 of the
+// group's largest is exact; a smaller one is off by at most 2^-39 of the
+// largest, less than FP32 sums of the products round.  Channels outside the
+// key are zero.
+__device__ __forceinline__ void query_halves(const CachedArgs& a, int c0, uint32_t (&q)[16], float& back) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint32_t w = 0;
+        const int j = c0 + 2 * i;
+        if (j >= a.ko && j < a.ko + a.R) w |= __ldg(a.q + j - a.ko);
+        if (j + 1 >= a.ko && j + 1 < a.ko + a.R) w |= static_cast<uint32_t>(__ldg(a.q + j + 1 - a.ko)) << 16;
+        q[i] = w;
+        m = __vmaxu2(m, w & 0x7fff7fffu);
+    }
+    const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent of the largest
+    const int sh = min(141 - e, 114);                                // 2^sh: largest to [2^14, 2^15)
+    const float up = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+    back = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 f = f2_get(f2_bf16(q[i]));
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(f.y * up), "f"(f.x * up));
+    }
+}
+
+template <int BITS, int NC, int W, bool NORM, bool LIVE>
+__global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(const CachedArgs a, const WidePlan pl) {
+    constexpr int CH = BITS / 4;                  // 16-byte chunks of codes a group
+    constexpr int K = BITS == 8 ? 2 : 4;          // rows of a block of dots
+    constexpr int TEAMS = wide_warps(NC) / W;     // tokens of the CTA at a time
+    extern __shared__ __align__(16) unsigned char dyn[];
+    const uint32_t sm = smem_u32(dyn);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int team = warp / W, w = warp % W;
+    const int SL = a.S + (LIVE ? 1 : 0), seg = pl.seg, nseg = (a.S + seg - 1) / seg;
+    const int groups = (a.D + 31) / 32, mine = min(groups - w * 32 * NC, 32 * NC);  // of this warp
+    const unsigned char** rows = reinterpret_cast<const unsigned char**>(dyn + pl.rows_at);
+    volatile int* abort = reinterpret_cast<volatile int*>(dyn + pl.abort_at);
+    unsigned char* own = dyn + pl.warp_at + warp * pl.warp_bytes;
+    unsigned char* own0 = dyn + pl.warp_at + team * W * pl.warp_bytes;  // of the team's first warp
+    const uint32_t bar = smem_u32(own) + pl.bar_at;
+    const uint32_t slots = smem_u32(own) + pl.coef_at + 128;
+    float* zbuf = reinterpret_cast<float*>(own + pl.z_at);    // logits, then 1 / RMS (of the team's first warp)
+    float* coef = reinterpret_cast<float*>(own + pl.coef_at);
+    if (threadIdx.x == 0) *abort = 0;
+    if (lane == 0) {
+        mbar_init(reinterpret_cast<uint64_t*>(own + pl.bar_at), 1);
+        mbar_fence_init();
+    }
+    for (int s = threadIdx.x; s < a.S; s += blockDim.x) rows[s] = a.rows[s];
+    pdl_wait();
+
+    // 8 bits: a lane's 32 bytes of codes are read as two halves, the second
+    // first where that keeps the lanes of a phase on different banks; its
+    // channels are then those halves in that order.
+    const int sw = BITS == 8 ? (lane >> 2) & 1 : 0;
+    uint32_t has = 0, keys = 0, whole = 0;  // bit c: the lane's group c exists, has key channels, has no others
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int c0 = (w * 32 * NC + c * 32 + lane) * 32;
+        if (c0 < a.D) has |= 1u << c;
+        if (c0 < a.D && c0 < a.ko + a.R && c0 + 32 > a.ko) keys |= 1u << c;
+        if (c0 >= a.ko && c0 + 32 <= a.ko + a.R) whole |= 1u << c;
+    }
+    const uint32_t any_keys = __reduce_or_sync(0xffffffffu, keys), all_whole = __reduce_and_sync(0xffffffffu, whole);
+    // channels of register pairs 0-7 and 8-15 of group c
+    auto chan = [&](int c, int i) { return (w * 32 * NC + c * 32 + lane) * 32 + 16 * (i ^ sw); };
+    if (team == 0) {  // the query, in the order of each lane's registers
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            uint32_t q[16];
+            float back;
+            query_halves(a, (w * 32 * NC + c * 32 + lane) * 32, q, back);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = 4 * (i ^ (2 * sw));
+                uint4 v;
+                v.x = k == 0 ? q[0] : k == 4 ? q[4] : k == 8 ? q[8] : q[12];
+                v.y = k == 0 ? q[1] : k == 4 ? q[5] : k == 8 ? q[9] : q[13];
+                v.z = k == 0 ? q[2] : k == 4 ? q[6] : k == 8 ? q[10] : q[14];
+                v.w = k == 0 ? q[3] : k == 4 ? q[7] : k == 8 ? q[11] : q[15];
+                sts128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16, v);
+            }
+            reinterpret_cast<float*>(dyn + pl.back_at)[(w * NC + c) * 32 + lane] = back;
+        }
+    }
+    __syncthreads();  // the last of the CTA's
+
+    // the lane's codes of group c in a slot; a lane without the group reads another's and uses nothing of it
+    uint32_t code_at[NC][CH], scale_at[NC];
+    bool cut = false;  // 8 bits: the lane's last group ends in its first half
+    int cut_c = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int g = min(c * 32 + lane, mine - 1);
+        const bool half_only = BITS == 8 && (w * 32 * NC + g) * 32 + 16 >= a.D;
+        if (half_only && (has >> c & 1u)) cut = true, cut_c = c;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) code_at[c][i] = slots + g * (16 * CH) + (CH == 2 && !half_only ? (i ^ sw) * 16 : 0);
+        scale_at[c] = slots + pl.scales + g;
+    }
+    auto codes = [&](uint32_t slot, int c) {
+        CacheCodes<BITS> x;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const uint4 u = lds128(code_at[c][i] + slot);
+            x.w[4 * i] = u.x, x.w[4 * i + 1] = u.y, x.w[4 * i + 2] = u.z, x.w[4 * i + 3] = u.w;
+        }
+        return x;
+    };
+    // bytes of this warp's part of a record, and its copy into slot r
+    const uint32_t code_bytes = W == 1 ? pl.slot : min(a.codes - w * pl.codes, pl.codes);
+    const uint32_t rec = W == 1 ? pl.slot : ((a.stat + 8 + 15) & ~15u);
+    const uint32_t scale_bytes = W == 1 ? 0 : min(rec - (a.codes + w * NC * 32), static_cast<uint32_t>(NC) * 32);
+    const uint32_t part_bytes = W == 1 ? pl.slot : code_bytes + scale_bytes + 16;
+    auto fetch = [&](long long n, int s, int r) {
+        const unsigned char* p = rows[s] + n * a.row_ld;
+        const uint32_t dst = slots + r * pl.slot;
+        bulk_load(dst, p + (W == 1 ? 0 : w * pl.codes), code_bytes, bar);
+        if constexpr (W > 1) {
+            bulk_load(dst + pl.scales, p + a.codes + w * NC * 32, scale_bytes, bar);
+            bulk_load(dst + pl.stat / 16 * 16, p + a.stat / 16 * 16, 16, bar);
+        }
+    };
+    auto expect = [&](int cnt) {
+        if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cnt * part_bytes) : "memory");
+        __syncwarp();
+    };
+    const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0;
+    const float inv_D = 1.0f / static_cast<float>(a.D), inv_R = 1.0f / static_cast<float>(a.R);
+    int flip = 0;
+    // sums over the team's warps of what lane-wise values `x` of each are (two warps; buffers in turn)
+    auto exchange = [&](float x) {
+        if constexpr (W > 1) {
+            float* r0 = reinterpret_cast<float*>(own0 + pl.red_at) + flip * 32;
+            float* r1 = reinterpret_cast<float*>(own0 + pl.warp_bytes + pl.red_at) + flip * 32;
+            (w ? r1 : r0)[lane] = x;
+            named_bar_sync(team + 1, 32 * W);
+            x = r0[lane] + r1[lane];
+            flip ^= 1;
+        }
+        return x;
+    };
+
+    const long long first = static_cast<long long>(blockIdx.x) * TEAMS + team, stride = static_cast<long long>(gridDim.x) * TEAMS;
+    uint32_t phase = 0, stuck_phase = 0;
+    bool stuck = false;  // a wait ran out (here or in another warp of the CTA): nothing more is fetched
+    if (first < a.N) {
+        const int cnt = min(seg, a.S);
+        expect(cnt);
+        if (lane < cnt) fetch(first, lane, lane);
+    }
+    for (long long n = first; n < a.N; n += stride) {
+        f2 acc[NC][16];
+        float mx, sum;
+        if constexpr (LIVE) {  // the live source first: it is the mixture, with weight 1
+            float p0 = 0.0f, p1 = 0.0f;
+            const uint16_t* x = a.live + n * a.live_ld;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = chan(c, i / 2) + 8 * (i & 1);
+                    const uint4 u = j < a.D ? ld_global_nc_v4(x + j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[c][4 * i + k] = f2_bf16(u4_get(u, k));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                if (!(any_keys >> c & 1u)) continue;
+                f2 d = 0ull, s2 = 0ull;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 q = lds128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const f2 v = acc[c][4 * i + k];
+                        d = f2_fma(v, f2_half(u4_get(q, k)), d);
+                        if (all_whole >> c & 1u) {
+                            s2 = f2_fma(v, v, s2);
+                        } else {
+                            const int j = chan(c, i / 2) + 8 * (i & 1) + 2 * k - a.ko;
+                            const float2 y = f2_get(v);
+                            s2 = f2_fma(v, f2_make(j >= 0 && j < a.R ? y.x : 0.0f, j + 1 >= 0 && j + 1 < a.R ? y.y : 0.0f), s2);
+                        }
+                    }
+                }
+                if (keys >> c & 1u) {
+                    p0 += f2_sum(d) * reinterpret_cast<const float*>(dyn + pl.back_at)[(w * NC + c) * 32 + lane];
+                    p1 += f2_sum(s2);
+                }
+            }
+            p0 = warp_sum(p0);
+            p1 = warp_sum(p1);
+            if constexpr (W > 1) {
+                const float both = exchange(lane == 0 ? p0 : p1);
+                p0 = __shfl_sync(0xffffffffu, both, 0);
+                p1 = __shfl_sync(0xffffffffu, both, 1);
+            }
+            const float rs = rsqrtf(p1 * inv_R + a.eps);
+            mx = a.scale * rs * p0;
+            sum = mx == mx ? 1.0f : mx;  // a NaN stays one
+            if (w == 0 && lane == 0) zbuf[a.S] = mx, zbuf[SL + a.S] = rs;
+        } else {
+            mx = __uint_as_float(0xff800000u);
+            sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c][i] = 0ull;
+            }
+        }
+        for (int g = 0; g < nseg; ++g) {
+            if (!mbar_wait_s(bar, phase, abort, &g_cached_wide_error, kSiteCached) && !stuck) stuck = true, stuck_phase = phase;
+            phase ^= 1u;
+            const int s0 = g * seg, cnt = min(seg, a.S - s0);
+            // what the slots take next
+            const bool last = g == nseg - 1;
+            const long long nn = last ? n + stride : n;
+            const int ns0 = last ? 0 : s0 + seg;
+            const int ncnt = nn < a.N && !*abort ? min(seg, a.S - ns0) : 0;
+            float* dotbuf = coef;
+            if (any_keys) {
+                auto dots = [&](auto count, int r0) {
+                    constexpr int M = decltype(count)::value;
+                    float p[M];
+#pragma unroll
+                    for (int r = 0; r < M; ++r) p[r] = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        if (!(any_keys >> c & 1u)) continue;
+                        uint4 q[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) q[i] = lds128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16);
+                        const float back = reinterpret_cast<const float*>(dyn + pl.back_at)[(w * NC + c) * 32 + lane];
+#pragma unroll
+                        for (int r = 0; r < M; ++r) {
+                            const uint32_t at = (r0 + r) * pl.slot;
+                            uint32_t h[16];
+                            codes(at, c).unpack(h);
+                            const float f = keys >> c & 1u ? cache_scale(lds8(scale_at[c] + at)) : 0.0f;
+                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                half2_dot(h[i], u4_get(q[i / 4], i % 4), d[0], d[1]);
+                                half2_dot(h[i + 1], u4_get(q[i / 4], i % 4 + 1), d[2], d[3]);
+                            }
+                            p[r] += ((d[0] + d[1]) + (d[2] + d[3])) * back * f;
+                        }
+                    }
+                    lanes_sum_to<32>(p, dotbuf + r0);
+                };
+                int r = 0;
+                if constexpr (K == 4) {
+                    for (; r + 4 <= cnt; r += 4) dots(std::integral_constant<int, 4>{}, r);
+                    if (r + 2 <= cnt) dots(std::integral_constant<int, 2>{}, r), r += 2;
+                } else {
+                    for (; r + 2 <= cnt; r += 2) dots(std::integral_constant<int, 2>{}, r);
+                }
+                if (r < cnt) dots(std::integral_constant<int, 1>{}, r);
+            } else {
+                dotbuf[lane] = 0.0f;
+            }
+            __syncwarp();
+            // logits and weights of the segment: lane s has row s
+            const float dot = exchange(lane < cnt ? dotbuf[lane] : 0.0f);
+            float z = __uint_as_float(0xff800000u);
+            if (lane < cnt) {
+                const uint32_t at = slots + lane * pl.slot + pl.stat;
+                const bool good = lds32(at + 4) == a.tag;
+                if (!good && w == 0) atomicCAS(&g_cached_wide_error, 0u, static_cast<unsigned>(kSiteCacheTag));
+                const float rs = good ? rsqrtf(__uint_as_float(lds32(at)) + a.eps) : __uint_as_float(0x7fc00000u);
+                z = a.scale * rs * dot;
+                if (w == 0) zbuf[s0 + lane] = z, zbuf[SL + s0 + lane] = rs;
+            }
+            const float mnew = fmaxf(mx, warp_max(z));
+            const float e = lane < cnt ? __expf(z - mnew) : 0.0f, corr = __expf(mx - mnew);
+            __syncwarp();
+            coef[lane] = e;
+            sum = sum * corr + warp_sum(e);
+            mx = mnew;
+            if (LIVE || g > 0) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c][i] = f2_mul(acc[c][i], f2_dup(corr));
+                }
+            }
+            if (ncnt) expect(ncnt);
+            else __syncwarp();
+            auto mix = [&](int r) {
+                const uint32_t at = r * pl.slot;
+                const float er = coef[r];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t h[16];
+                    codes(at, c).unpack(h);
+                    const float f = er * cache_scale(lds8(scale_at[c] + at));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c][i] = f2_fma(f2_half(h[i]), f2_dup(f), acc[c][i]);
+                }
+            };
+            int r = 0;
+            for (; r + 2 <= cnt; r += 2) {
+                mix(r);
+                mix(r + 1);
+                read_done(acc[NC - 1][15]);  // both slots are read: they take the next segment's records
+                if (lane < 2 && r + lane < ncnt) fetch(nn, ns0 + r + lane, r + lane);
+            }
+            if (r < cnt) {
+                mix(r);
+                read_done(acc[NC - 1][15]);
+            }
+            if (r + lane < ncnt) fetch(nn, ns0 + r + lane, r + lane);
+        }
+        const float inv = 1.0f / sum;
+        float post = inv;
+        if constexpr (NORM) {
+            if (BITS == 8 && cut) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c == cut_c && i / 8 != sw) acc[c][i] = 0ull;
+                }
+            }
+            float s1 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                f2 ss = 0ull;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ss = f2_fma(acc[c][i], acc[c][i], ss);
+                if (has >> c & 1u) s1 += f2_sum(ss);
+            }
+            s1 = exchange(warp_sum(s1));
+            const float o_rstd = rsqrtf(s1 * inv * inv * inv_D + a.eps);
+            if (w == 0 && lane == 0) a.o_rstd[n] = o_rstd;
+            post *= o_rstd;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (NORM) {
+                    const int j = chan(c, i / 2) + 8 * (i & 1);
+                    const uint4 u = j < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + j)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[4 * i + k] = f2_to_bf16(f2_mul(f2_mul(acc[c][4 * i + k], f2_dup(post)), f2_bf16(u4_get(u, k))));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[4 * i + k] = f2_to_bf16(f2_mul(acc[c][4 * i + k], f2_dup(post)));
+                }
+            }
+            const int half[2] = {chan(c, 0), chan(c, 1)};
+            store_halves(a.y + n * a.D, half, a.D, wide, o);
+        }
+        if (w == 0) {
+            __syncwarp();
+            for (int s = lane; s < SL; s += 32) {
+                const float z = zbuf[s];
+                a.logit[n * SL + s] = z;
+                a.rstd[n * SL + s] = zbuf[SL + s];
+                a.alpha[n * SL + s] = __expf(z - mx) * inv;
+            }
+            __syncwarp();
+        }
+    }
+    if (stuck) {  // leave no copy of this warp's in flight
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test_sleep_s(bar, stuck_phase, 20000u))
+            if (global_timer_ns() - t0 > kWaitLimitNs) break;
+    }
+}
+
+template <int BITS, int NC, int W>
+cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
+    const WidePlan p = wide_plan(a.D, a.S, a.live != nullptr, BITS, NC, W);
+    auto run = [&](auto norm, auto live) {
+        constexpr auto kern = cached_wide_kernel<BITS, NC, W, decltype(norm)::value, decltype(live)::value>;
+        int fit = 0;
+        const cudaError_t err = kernel_fit<kern>(32 * wide_warps(NC), p.smem, &fit);
+        if (err != cudaSuccess) return err;
+        const long long teams = wide_warps(NC) / W, want = (a.N + teams - 1) / teams;
+        return launch_pdl(kern, dim3(static_cast<unsigned>(want < sm_count ? want : sm_count)), dim3(32 * wide_warps(NC)), p.smem,
+                          stream, a, p);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    return a.w_o ? (a.live ? run(Yes{}, Yes{}) : run(Yes{}, No{})) : (a.live ? run(No{}, Yes{}) : run(No{}, No{}));
+}
+
+template <int BITS>
+cudaError_t launch_bits(const CachedArgs& a, int sm_count, cudaStream_t stream) {
+    const int groups = (a.D + 31) / 32;
+    if (groups <= 32) return launch_t<BITS, 1, 1>(a, sm_count, stream);
+    if (groups <= 64) return launch_t<BITS, 2, 1>(a, sm_count, stream);
+    if (groups <= 96) return launch_t<BITS, 3, 1>(a, sm_count, stream);
+    if (groups <= 128) return launch_t<BITS, 4, 1>(a, sm_count, stream);
+    if (groups <= 192) return launch_t<BITS, 3, 2>(a, sm_count, stream);
+    return launch_t<BITS, 4, 2>(a, sm_count, stream);
+}
+
+inline unsigned take_error() {
+    unsigned v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_cached_wide_error, sizeof v) != cudaSuccess) return 0xffffffffu;
+    if (v) cudaMemcpyToSymbol(g_cached_wide_error, &zero, sizeof zero);
+    return v;
+}
+
+}  // namespace
+}  // namespace attnres

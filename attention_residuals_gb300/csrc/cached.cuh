@@ -218,6 +218,11 @@ cudaError_t launch_cached_fwd(const CachedArgs& a, int bits, int sm_count, cudaS
 int cached_bwd_grid(int S, bool live, long long N, int D, int bits, int sm_count);
 cudaError_t launch_cached_bwd(CachedBwdArgs& a, int bits, int grid, int sm_count, cudaStream_t stream);
 unsigned take_cache_rows_error();
+// many tokens of rows of more than 512 channels: a warp or two a token (attnres_cached_wide.cuh)
+cudaError_t launch_cached_wide8(const CachedArgs& a, int sm_count, cudaStream_t stream);
+cudaError_t launch_cached_wide4(const CachedArgs& a, int sm_count, cudaStream_t stream);
+unsigned take_cached_wide8_error();
+unsigned take_cached_wide4_error();
 unsigned take_cached_fwd_error();
 
 }  // namespace attnres

@@ -182,4 +182,22 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* p, int left, bool wide, 
     }
 }
 
+// The same from two runs of 16 channels, at channels half[0] and half[1] of a row.
+__device__ __forceinline__ void store_halves(uint16_t* row, const int (&half)[2], int D, bool wide, const uint32_t (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint16_t* p = row + half[i];
+        if (wide) {
+            if (half[i] < D)
+                asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[8 * i]),
+                             "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                             "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                             : "memory");
+        } else {
+            if (half[i] < D) st_global_cs_v4(p, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]));
+            if (half[i] + 8 < D) st_global_cs_v4(p + 8, make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]));
+        }
+    }
+}
+
 }  // namespace attnres

@@ -34,6 +34,7 @@ enum WaitSite : unsigned {
     kSiteBwdExchange = 8,  // a cluster peer's partial sums did not arrive
     kSiteBounds = 9,       // debug build: a store's indices fell outside the call's sizes
     kSiteCacheTag = 10,    // a cache record's tag is not the call's
+    kSiteCached = 11,      // records of the compressed cache did not arrive
 };
 
 // Debug build (-DATTNRES_DEBUG, a stand-in for a memory checker): a global
