@@ -144,7 +144,6 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int team = warp / W, w = warp % W;
     const int SL = a.S + (LIVE ? 1 : 0), seg = pl.seg, nseg = (a.S + seg - 1) / seg;
-    const int groups = (a.D + 31) / 32, mine = min(groups - w * 32 * NC, 32 * NC);  // of this warp
     const unsigned char** rows = reinterpret_cast<const unsigned char**>(dyn + pl.rows_at);
     volatile int* abort = reinterpret_cast<volatile int*>(dyn + pl.abort_at);
     unsigned char* own = dyn + pl.warp_at + warp * pl.warp_bytes;
@@ -203,9 +202,9 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
     int cut_c = 0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int g = min(c * 32 + lane, mine - 1);
-        const bool half_only = BITS == 8 && (w * 32 * NC + g) * 32 + 16 >= a.D;
-        if (half_only && (has >> c & 1u)) cut = true, cut_c = c;
+        const int g = has >> c & 1u ? c * 32 + lane : 0;
+        const bool half_only = BITS == 8 && (has >> c & 1u) && (w * 32 * NC + g) * 32 + 16 >= a.D;
+        if (half_only) cut = true, cut_c = c;
 #pragma unroll
         for (int i = 0; i < CH; ++i) code_at[c][i] = slots + g * (16 * CH) + (CH == 2 && !half_only ? (i ^ sw) * 16 : 0);
         scale_at[c] = slots + pl.scales + g;
@@ -339,9 +338,14 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                     float p[M];
 #pragma unroll
                     for (int r = 0; r < M; ++r) p[r] = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c) {  // a loop: unrolled, the kernel would not stay in the instruction cache
                         if (!(any_keys >> c & 1u)) continue;
+                        const uint32_t g0 = has >> c & 1u ? c * 32 + lane : 0u;
+                        const bool half_only = cut && c == cut_c;
+                        uint32_t from[CH];
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) from[i] = slots + g0 * (16 * CH) + (CH == 2 && !half_only ? (i ^ sw) * 16 : 0);
                         uint4 q[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) q[i] = lds128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16);
@@ -349,9 +353,15 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
 #pragma unroll
                         for (int r = 0; r < M; ++r) {
                             const uint32_t at = (r0 + r) * pl.slot;
+                            CacheCodes<BITS> x;
+#pragma unroll
+                            for (int i = 0; i < CH; ++i) {
+                                const uint4 u = lds128(from[i] + at);
+                                x.w[4 * i] = u.x, x.w[4 * i + 1] = u.y, x.w[4 * i + 2] = u.z, x.w[4 * i + 3] = u.w;
+                            }
                             uint32_t h[16];
-                            codes(at, c).unpack(h);
-                            const float f = keys >> c & 1u ? cache_scale(lds8(scale_at[c] + at)) : 0.0f;
+                            x.unpack(h);
+                            const float f = keys >> c & 1u ? cache_scale(lds8(slots + pl.scales + g0 + at)) : 0.0f;
                             float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
@@ -414,9 +424,10 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                 }
             };
             int r = 0;
+#pragma unroll 1
             for (; r + 2 <= cnt; r += 2) {
-                mix(r);
-                mix(r + 1);
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) mix(r + u);
                 read_done(acc[NC - 1][15]);  // both slots are read: they take the next segment's records
                 if (lane < 2 && r + lane < ncnt) fetch(nn, ns0 + r + lane, r + lane);
             }
