@@ -28,7 +28,7 @@ __device__ unsigned g_cached_wide_error;
 
 // Warps of the one CTA an SM runs, by groups a lane: a multiple of the four
 // schedulers whose registers hold the mixture (32 a group) without spilling.
-__host__ __device__ constexpr int wide_warps(int nc) { return nc == 4 ? 8 : nc == 1 ? 20 : 12; }
+__host__ __device__ constexpr int wide_warps(int nc) { return nc == 4 ? 8 : nc == 1 ? 20 : nc == 2 ? 16 : 12; }
 constexpr int kWideSmem = 227 * 1024;
 
 struct WidePlan {
@@ -36,7 +36,7 @@ struct WidePlan {
     uint32_t slot;            // bytes of a slot: the warp's part of a record
     uint32_t codes, scales;   // of a slot: bytes of codes, where the scales begin
     uint32_t stat;            // where the statistic is in a slot
-    uint32_t q_at, back_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
+    uint32_t q_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
     uint32_t red_at, coef_at, z_at, bar_at;                         // in a warp's
     size_t smem;
 };
@@ -61,23 +61,24 @@ WidePlan wide_plan(int D, int S, bool live, int bits, int nc, int w) {
         return at;
     };
     p.q_at = take(nc * w * 32 * 64);
-    p.back_at = take(nc * w * 32 * 4);
     p.rows_at = take(S * 8);
-    p.abort_at = take(16);
+    p.abort_at = take(32);  // and the query's factor
     p.warp_at = off;
     off = 0;
     p.bar_at = take(16);
     p.z_at = take(2 * SL * 4);
     p.red_at = take(2 * 32 * 4);
     p.coef_at = take(32 * 4);
-    const uint32_t room = (kWideSmem - p.warp_at) / warps - off - 16;
+    // lanes behind a row's last group read on from its end
+    const uint32_t lanes = static_cast<uint32_t>(nc) * 32 * 4 * bits, over = lanes > p.slot ? lanes - p.slot : 0;
+    const uint32_t room = (kWideSmem - p.warp_at - over) / warps - off - 16;
     int most = static_cast<int>(room / p.slot);
     if (most > 30) most = 30;
     if (most < 1) most = 1;
     const int n = (S + most - 1) / most;
     p.seg = (S + n - 1) / n;
     p.warp_bytes = off + ((p.seg * p.slot + 15) & ~15u);
-    p.smem = p.warp_at + static_cast<size_t>(warps) * p.warp_bytes;
+    p.smem = p.warp_at + static_cast<size_t>(warps) * p.warp_bytes + over;
     return p;
 }
 
@@ -106,31 +107,18 @@ __device__ __forceinline__ void read_done(f2 v) {
     __syncwarp();
 }
 
-// The query's channels of one group as halves, scaled by a power of two that
-// puts the largest magnitude in [2^14, 2^15) (`back` undoes it).  bf16 has
-// fewer significand bits than a half, so every channel down to 2^-28 of the
-// group's largest is exact; a smaller one is off by at most 2^-39 of the
-// largest, less than FP32 sums of the products round.  Channels outside the
-// key are zero.
-__device__ __forceinline__ void query_halves(const CachedArgs& a, int c0, uint32_t (&q)[16], float& back) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        uint32_t w = 0;
-        const int j = c0 + 2 * i;
-        if (j >= a.ko && j < a.ko + a.R) w |= __ldg(a.q + j - a.ko);
-        if (j + 1 >= a.ko && j + 1 < a.ko + a.R) w |= static_cast<uint32_t>(__ldg(a.q + j + 1 - a.ko)) << 16;
-        q[i] = w;
-        m = __vmaxu2(m, w & 0x7fff7fffu);
-    }
-    const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent of the largest
-    const int sh = min(141 - e, 114);                                // 2^sh: largest to [2^14, 2^15)
+// The query's channels c0 .. c0 + 31 as halves times 2^sh, zero outside the
+// key.  sh puts the query's largest magnitude in [2^14, 2^15).  bf16 has fewer
+// significand bits than a half, so every channel down to 2^-28 of the largest
+// is exact; a smaller one is off by at most 2^-39 of the largest.
+__device__ __forceinline__ void query_halves(const CachedArgs& a, int c0, int sh, uint32_t (&q)[16]) {
     const float up = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-    back = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const float2 f = f2_get(f2_bf16(q[i]));
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(f.y * up), "f"(f.x * up));
+        const int j = c0 + 2 * i - a.ko;
+        const float x = j >= 0 && j < a.R ? bf16_bits_to_float(__ldg(a.q + j)) : 0.0f;
+        const float y = j + 1 >= 0 && j + 1 < a.R ? bf16_bits_to_float(__ldg(a.q + j + 1)) : 0.0f;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(y * up), "f"(x * up));
     }
 }
 
@@ -175,12 +163,23 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
     const uint32_t any_keys = __reduce_or_sync(0xffffffffu, keys), all_whole = __reduce_and_sync(0xffffffffu, whole);
     // channels of register pairs 0-7 and 8-15 of group c
     auto chan = [&](int c, int i) { return (w * 32 * NC + c * 32 + lane) * 32 + 16 * (i ^ sw); };
+    {  // the largest magnitude of the query, as bf16 bits
+        uint32_t m = 0;
+        for (int j = threadIdx.x; j < a.R; j += blockDim.x) m = max(m, static_cast<uint32_t>(__ldg(a.q + j)) & 0x7fffu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) reinterpret_cast<uint32_t*>(own + pl.coef_at)[0] = m;
+    }
+    __syncthreads();
+    uint32_t top = 0;
+    for (int i = lane; i < wide_warps(NC); i += 32)
+        top = max(top, *reinterpret_cast<const uint32_t*>(dyn + pl.warp_at + i * pl.warp_bytes + pl.coef_at));
+    const int sh = min(141 - static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7), 114);
+    const float back = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
     if (team == 0) {  // the query, in the order of each lane's registers
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             uint32_t q[16];
-            float back;
-            query_halves(a, (w * 32 * NC + c * 32 + lane) * 32, q, back);
+            query_halves(a, (w * 32 * NC + c * 32 + lane) * 32, sh, q);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int k = 4 * (i ^ (2 * sw));
@@ -191,30 +190,26 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                 v.w = k == 0 ? q[3] : k == 4 ? q[7] : k == 8 ? q[11] : q[15];
                 sts128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16, v);
             }
-            reinterpret_cast<float*>(dyn + pl.back_at)[(w * NC + c) * 32 + lane] = back;
         }
     }
     __syncthreads();  // the last of the CTA's
 
-    // the lane's codes of group c in a slot; a lane without the group reads another's and uses nothing of it
-    uint32_t code_at[NC][CH], scale_at[NC];
-    bool cut = false;  // 8 bits: the lane's last group ends in its first half
-    int cut_c = 0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int g = has >> c & 1u ? c * 32 + lane : 0;
-        const bool half_only = BITS == 8 && (has >> c & 1u) && (w * 32 * NC + g) * 32 + 16 >= a.D;
-        if (half_only) cut = true, cut_c = c;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) code_at[c][i] = slots + g * (16 * CH) + (CH == 2 && !half_only ? (i ^ sw) * 16 : 0);
-        scale_at[c] = slots + pl.scales + g;
-    }
-    auto codes = [&](uint32_t slot, int c) {
+    // Where the lane's codes and scale of group 0 lie in slot 0.  Lanes behind
+    // the row's last group read on, whatever is there, and use nothing of it.
+    const uint32_t code0 = slots + lane * (16 * CH) + 16 * sw, code1 = slots + lane * 32 + 16 * (1 - sw);  // (8 bits)
+    const uint32_t scale0 = slots + pl.scales + lane;
+    // 8 bits: the lane's last group ends in its first half, the second is not codes
+    const bool cut = BITS == 8 && a.D % 32 != 0 && a.D % 32 <= 16 &&
+                     a.D / 32 >= w * 32 * NC && a.D / 32 < (w + 1) * 32 * NC && a.D / 32 % 32 == lane;
+    const int cut_c = a.D / 32 / 32 - w * NC;
+    const bool any_cut = BITS == 8 && a.D % 32 != 0 && a.D % 32 <= 16;
+    auto codes = [&](uint32_t at, int c) {
         CacheCodes<BITS> x;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const uint4 u = lds128(code_at[c][i] + slot);
-            x.w[4 * i] = u.x, x.w[4 * i + 1] = u.y, x.w[4 * i + 2] = u.z, x.w[4 * i + 3] = u.w;
+        const uint4 u = lds128(code0 + at + c * (512 * CH));
+        x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w;
+        if constexpr (CH == 2) {
+            const uint4 v = lds128(code1 + at + c * (512 * CH));
+            x.w[4] = v.x, x.w[5] = v.y, x.w[6] = v.z, x.w[7] = v.w;
         }
         return x;
     };
@@ -240,14 +235,15 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
     const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0;
     const float inv_D = 1.0f / static_cast<float>(a.D), inv_R = 1.0f / static_cast<float>(a.R);
     int flip = 0;
-    // sums over the team's warps of what lane-wise values `x` of each are (two warps; buffers in turn)
+    // sums over the team's warps of what lane-wise values `x` of each are (buffers in turn)
     auto exchange = [&](float x) {
         if constexpr (W > 1) {
-            float* r0 = reinterpret_cast<float*>(own0 + pl.red_at) + flip * 32;
-            float* r1 = reinterpret_cast<float*>(own0 + pl.warp_bytes + pl.red_at) + flip * 32;
-            (w ? r1 : r0)[lane] = x;
+            const unsigned char* r = own0 + pl.red_at + (flip * 32 + lane) * 4;
+            *reinterpret_cast<float*>(own + pl.red_at + (flip * 32 + lane) * 4) = x;
             named_bar_sync(team + 1, 32 * W);
-            x = r0[lane] + r1[lane];
+            x = *reinterpret_cast<const float*>(r);
+#pragma unroll
+            for (int u = 1; u < W; ++u) x += *reinterpret_cast<const float*>(r + u * pl.warp_bytes);
             flip ^= 1;
         }
         return x;
@@ -297,10 +293,7 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                         }
                     }
                 }
-                if (keys >> c & 1u) {
-                    p0 += f2_sum(d) * reinterpret_cast<const float*>(dyn + pl.back_at)[(w * NC + c) * 32 + lane];
-                    p1 += f2_sum(s2);
-                }
+                if (keys >> c & 1u) p0 += f2_sum(d) * back, p1 += f2_sum(s2);
             }
             p0 = warp_sum(p0);
             p1 = warp_sum(p1);
@@ -336,39 +329,36 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                 auto dots = [&](auto count, int r0) {
                     constexpr int M = decltype(count)::value;
                     float p[M];
+                    uint32_t at[M];
 #pragma unroll
-                    for (int r = 0; r < M; ++r) p[r] = 0.0f;
+                    for (int r = 0; r < M; ++r) p[r] = 0.0f, at[r] = (r0 + r) * pl.slot;
 #pragma unroll 1
                     for (int c = 0; c < NC; ++c) {  // a loop: unrolled, the kernel would not stay in the instruction cache
                         if (!(any_keys >> c & 1u)) continue;
-                        const uint32_t g0 = has >> c & 1u ? c * 32 + lane : 0u;
-                        const bool half_only = cut && c == cut_c;
-                        uint32_t from[CH];
-#pragma unroll
-                        for (int i = 0; i < CH; ++i) from[i] = slots + g0 * (16 * CH) + (CH == 2 && !half_only ? (i ^ sw) * 16 : 0);
+                        const bool key = keys >> c & 1u;
                         uint4 q[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) q[i] = lds128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16);
-                        const float back = reinterpret_cast<const float*>(dyn + pl.back_at)[(w * NC + c) * 32 + lane];
+                        CacheCodes<BITS> x[M];
+                        float f[M];
+#pragma unroll
+                        for (int r = 0; r < M; ++r) x[r] = codes(at[r], c), f[r] = cache_scale(lds8(scale0 + at[r] + c * 32));
+                        if (any_cut && cut && c == cut_c) {
+#pragma unroll
+                            for (int r = 0; r < M; ++r) {
+#pragma unroll
+                                for (int i = 0; i < BITS; ++i)
+                                    if (i / 4 != sw) x[r].w[i] = 0u;
+                            }
+                        }
 #pragma unroll
                         for (int r = 0; r < M; ++r) {
-                            const uint32_t at = (r0 + r) * pl.slot;
-                            CacheCodes<BITS> x;
-#pragma unroll
-                            for (int i = 0; i < CH; ++i) {
-                                const uint4 u = lds128(from[i] + at);
-                                x.w[4 * i] = u.x, x.w[4 * i + 1] = u.y, x.w[4 * i + 2] = u.z, x.w[4 * i + 3] = u.w;
-                            }
                             uint32_t h[16];
-                            x.unpack(h);
-                            const float f = keys >> c & 1u ? cache_scale(lds8(slots + pl.scales + g0 + at)) : 0.0f;
-                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            x[r].unpack(h);
+                            float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                half2_dot(h[i], u4_get(q[i / 4], i % 4), d[0], d[1]);
-                                half2_dot(h[i + 1], u4_get(q[i / 4], i % 4 + 1), d[2], d[3]);
-                            }
-                            p[r] += ((d[0] + d[1]) + (d[2] + d[3])) * back * f;
+                            for (int i = 0; i < 16; ++i) half2_dot(h[i], u4_get(q[i / 4], i % 4), d0, d1);
+                            p[r] += key ? (d0 + d1) * f[r] : 0.0f;
                         }
                     }
                     lanes_sum_to<32>(p, dotbuf + r0);
@@ -386,7 +376,7 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
             }
             __syncwarp();
             // logits and weights of the segment: lane s has row s
-            const float dot = exchange(lane < cnt ? dotbuf[lane] : 0.0f);
+            const float dot = exchange(lane < cnt ? dotbuf[lane] : 0.0f) * back;
             float z = __uint_as_float(0xff800000u);
             if (lane < cnt) {
                 const uint32_t at = slots + lane * pl.slot + pl.stat;
@@ -418,7 +408,7 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                 for (int c = 0; c < NC; ++c) {
                     uint32_t h[16];
                     codes(at, c).unpack(h);
-                    const float f = er * cache_scale(lds8(scale_at[c] + at));
+                    const float f = er * cache_scale(lds8(scale0 + at + c * 32));
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[c][i] = f2_fma(f2_half(h[i]), f2_dup(f), acc[c][i]);
                 }
@@ -440,7 +430,7 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
         const float inv = 1.0f / sum;
         float post = inv;
         if constexpr (NORM) {
-            if (BITS == 8 && cut) {
+            if (any_cut && cut) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
 #pragma unroll
@@ -521,9 +511,9 @@ cudaError_t launch_bits(const CachedArgs& a, int sm_count, cudaStream_t stream) 
     if (groups <= 32) return launch_t<BITS, 1, 1>(a, sm_count, stream);
     if (groups <= 64) return launch_t<BITS, 2, 1>(a, sm_count, stream);
     if (groups <= 96) return launch_t<BITS, 3, 1>(a, sm_count, stream);
-    if (groups <= 128) return launch_t<BITS, 4, 1>(a, sm_count, stream);
+    if (groups <= 128) return launch_t<BITS, 2, 2>(a, sm_count, stream);
     if (groups <= 192) return launch_t<BITS, 3, 2>(a, sm_count, stream);
-    return launch_t<BITS, 4, 2>(a, sm_count, stream);
+    return launch_t<BITS, 2, 4>(a, sm_count, stream);
 }
 
 inline unsigned take_error() {
