@@ -26,9 +26,6 @@ namespace {
 
 __device__ unsigned g_cached_wide_error;
 
-// Warps of the one CTA an SM runs, by groups a lane: a multiple of the four
-// schedulers whose registers hold the mixture (32 a group) without spilling.
-__host__ __device__ constexpr int wide_warps(int nc) { return nc == 4 ? 8 : nc == 1 ? 20 : nc == 2 ? 16 : 12; }
 constexpr int kWideSmem = 227 * 1024;
 
 struct WidePlan {
@@ -36,15 +33,15 @@ struct WidePlan {
     uint32_t slot;            // bytes of a slot: the warp's part of a record
     uint32_t codes, scales;   // of a slot: bytes of codes, where the scales begin
     uint32_t stat;            // where the statistic is in a slot
-    uint32_t q_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
+    uint32_t q_at, w_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
     uint32_t red_at, coef_at, z_at, bar_at;                         // in a warp's
     size_t smem;
 };
 
-WidePlan wide_plan(int D, int S, bool live, int bits, int nc, int w) {
+WidePlan wide_plan(int D, int S, bool live, bool norm, int bits, int nc, int w, int warps) {
     WidePlan p{};
     const uint32_t rec = cache_row_bytes(D, bits), codes = cache_code_bytes(D, bits), stat = cache_stat_offset(D, bits);
-    const int SL = S + (live ? 1 : 0), warps = wide_warps(nc);
+    const int SL = S + (live ? 1 : 0);
     if (w == 1) {
         p.slot = rec;
         p.codes = p.scales = codes;
@@ -61,6 +58,7 @@ WidePlan wide_plan(int D, int S, bool live, int bits, int nc, int w) {
         return at;
     };
     p.q_at = take(nc * w * 32 * 64);
+    p.w_at = take(norm ? nc * w * 32 * 64 : 0);
     p.rows_at = take(S * 8);
     p.abort_at = take(32);  // and the query's factor
     p.warp_at = off;
@@ -122,11 +120,11 @@ __device__ __forceinline__ void query_halves(const CachedArgs& a, int c0, int sh
     }
 }
 
-template <int BITS, int NC, int W, bool NORM, bool LIVE>
-__global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(const CachedArgs a, const WidePlan pl) {
+template <int BITS, int NC, int W, int WARPS, bool NORM, bool LIVE>
+__global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const CachedArgs a, const WidePlan pl) {
     constexpr int CH = BITS / 4;                  // 16-byte chunks of codes a group
     constexpr int K = BITS == 8 ? 2 : 4;          // rows of a block of dots
-    constexpr int TEAMS = wide_warps(NC) / W;     // tokens of the CTA at a time
+    constexpr int TEAMS = WARPS / W;     // tokens of the CTA at a time
     extern __shared__ __align__(16) unsigned char dyn[];
     const uint32_t sm = smem_u32(dyn);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -171,11 +169,11 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
     }
     __syncthreads();
     uint32_t top = 0;
-    for (int i = lane; i < wide_warps(NC); i += 32)
+    for (int i = lane; i < WARPS; i += 32)
         top = max(top, *reinterpret_cast<const uint32_t*>(dyn + pl.warp_at + i * pl.warp_bytes + pl.coef_at));
     const int sh = min(141 - static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7), 114);
     const float back = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-    if (team == 0) {  // the query, in the order of each lane's registers
+    if (team == 0) {  // the query and the output's weight, in the order of each lane's registers
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             uint32_t q[16];
@@ -189,6 +187,11 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
                 v.z = k == 0 ? q[2] : k == 4 ? q[6] : k == 8 ? q[10] : q[14];
                 v.w = k == 0 ? q[3] : k == 4 ? q[7] : k == 8 ? q[11] : q[15];
                 sts128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16, v);
+                if constexpr (NORM) {
+                    const int j = chan(c, i / 2) + 8 * (i & 1);
+                    sts128(sm + pl.w_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16,
+                           j < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + j)) : make_uint4(0u, 0u, 0u, 0u));
+                }
             }
         }
     }
@@ -457,8 +460,7 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (NORM) {
-                    const int j = chan(c, i / 2) + 8 * (i & 1);
-                    const uint4 u = j < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + j)) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 u = lds128(sm + pl.w_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         o[4 * i + k] = f2_to_bf16(f2_mul(f2_mul(acc[c][4 * i + k], f2_dup(post)), f2_bf16(u4_get(u, k))));
@@ -488,16 +490,16 @@ __global__ void __launch_bounds__(32 * wide_warps(NC), 1) cached_wide_kernel(con
     }
 }
 
-template <int BITS, int NC, int W>
+template <int BITS, int NC, int W, int WARPS>
 cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
-    const WidePlan p = wide_plan(a.D, a.S, a.live != nullptr, BITS, NC, W);
+    const WidePlan p = wide_plan(a.D, a.S, a.live != nullptr, a.w_o != nullptr, BITS, NC, W, WARPS);
     auto run = [&](auto norm, auto live) {
-        constexpr auto kern = cached_wide_kernel<BITS, NC, W, decltype(norm)::value, decltype(live)::value>;
+        constexpr auto kern = cached_wide_kernel<BITS, NC, W, WARPS, decltype(norm)::value, decltype(live)::value>;
         int fit = 0;
-        const cudaError_t err = kernel_fit<kern>(32 * wide_warps(NC), p.smem, &fit);
+        const cudaError_t err = kernel_fit<kern>(32 * WARPS, p.smem, &fit);
         if (err != cudaSuccess) return err;
-        const long long teams = wide_warps(NC) / W, want = (a.N + teams - 1) / teams;
-        return launch_pdl(kern, dim3(static_cast<unsigned>(want < sm_count ? want : sm_count)), dim3(32 * wide_warps(NC)), p.smem,
+        const long long teams = WARPS / W, want = (a.N + teams - 1) / teams;
+        return launch_pdl(kern, dim3(static_cast<unsigned>(want < sm_count ? want : sm_count)), dim3(32 * WARPS), p.smem,
                           stream, a, p);
     };
     using Yes = std::true_type;
@@ -508,12 +510,17 @@ cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
 template <int BITS>
 cudaError_t launch_bits(const CachedArgs& a, int sm_count, cudaStream_t stream) {
     const int groups = (a.D + 31) / 32;
-    if (groups <= 32) return launch_t<BITS, 1, 1>(a, sm_count, stream);
-    if (groups <= 64) return launch_t<BITS, 2, 1>(a, sm_count, stream);
-    if (groups <= 96) return launch_t<BITS, 3, 1>(a, sm_count, stream);
-    if (groups <= 128) return launch_t<BITS, 2, 2>(a, sm_count, stream);
-    if (groups <= 192) return launch_t<BITS, 3, 2>(a, sm_count, stream);
-    return launch_t<BITS, 2, 4>(a, sm_count, stream);
+    // groups a lane, warps a token, warps of an SM (as many as the registers
+    // allow without spilling).  Measured, output norm: S=10 N=32768 D=4096,
+    // 4 bits 318 us with <4, 1, 8> against 320 (2, 2, 16) and 351 (2, 2, 12),
+    // 8 bits 387 against 401 and 432; S=64 N=8192 D=8192, 4 bits 904 with
+    // <2, 4, 16> against 956 (4, 2, 8) and 941 (2, 4, 12).
+    if (groups <= 32) return launch_t<BITS, 1, 1, 20>(a, sm_count, stream);
+    if (groups <= 64) return launch_t<BITS, 2, 1, 16>(a, sm_count, stream);
+    if (groups <= 96) return launch_t<BITS, 3, 1, 12>(a, sm_count, stream);
+    if (groups <= 128) return launch_t<BITS, 4, 1, 8>(a, sm_count, stream);
+    if (groups <= 192) return launch_t<BITS, 2, 3, 15>(a, sm_count, stream);
+    return launch_t<BITS, 2, 4, 16>(a, sm_count, stream);
 }
 
 inline unsigned take_error() {
