@@ -8,6 +8,7 @@
 // block into the FP32 mixture while its half pairs are still in registers.
 // The key statistic of a cached row is read from its record; the live bf16
 // source, read last, gets its own.
+#include <cstdlib>
 #include <type_traits>
 
 #include "cached_stage.cuh"
@@ -361,7 +362,9 @@ unsigned take_cached_fwd_error() {
 }
 
 cudaError_t launch_cached_fwd(const CachedArgs& a, int bits, int sm_count, cudaStream_t stream) {
-    if (cached_team(a.D) >= 32 && a.N >= kWideTokens)
+    const char* form = std::getenv("ATTNRES_CACHED_FWD");  // "warp" or "cta": one form wherever it fits (tests)
+    const bool wide = form && form[0] == 'w' ? true : form && form[0] == 'c' ? false : a.N >= kWideTokens;
+    if (cached_team(a.D) >= 32 && wide)
         return bits == 8 ? launch_cached_wide8(a, sm_count, stream) : launch_cached_wide4(a, sm_count, stream);
     return bits == 8 ? launch_bits<8>(a, sm_count, stream) : launch_bits<4>(a, sm_count, stream);
 }
