@@ -892,13 +892,14 @@ attnres_status attnres_check_device_error(void) {
     const unsigned mg2 = take_multi_grad_mma_error();
     const unsigned cr = take_cache_rows_error();
     const unsigned cf = take_cached_fwd_error();
+    const unsigned cb = take_cached_bwd_error();
     const unsigned cw8 = take_cached_wide8_error();
     const unsigned cw4 = take_cached_wide4_error();
     if (f == 0xffffffffu || b == 0xffffffffu || mf == 0xffffffffu || mb == 0xffffffffu || mg == 0xffffffffu ||
-        mm == 0xffffffffu || mg2 == 0xffffffffu || cr == 0xffffffffu || cf == 0xffffffffu ||
+        mm == 0xffffffffu || mg2 == 0xffffffffu || cr == 0xffffffffu || cf == 0xffffffffu || cb == 0xffffffffu ||
         cw8 == 0xffffffffu || cw4 == 0xffffffffu)
         return ATTNRES_ERR_CUDA;
-    return (f || b || mf || mb || mg || mm || mg2 || cr || cf || cw8 || cw4) ? ATTNRES_ERR_DEVICE : ATTNRES_OK;
+    return (f || b || mf || mb || mg || mm || mg2 || cr || cf || cb || cw8 || cw4) ? ATTNRES_ERR_DEVICE : ATTNRES_OK;
 }
 
 // ---------------------------------------------------------------------------

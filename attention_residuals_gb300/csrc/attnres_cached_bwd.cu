@@ -24,28 +24,31 @@
 namespace attnres {
 namespace {
 
+__device__ unsigned g_cached_bwd_error;
+
 constexpr int kBwdThreads = 256;      // threads of an SM (up to 255 registers each)
 constexpr int kSmemSm = 227 * 1024;   // shared memory of an SM that CTAs can have
 constexpr int kResidentWarp = 28 << 10;  // a warp's shared memory up to which whole tokens are kept (8 warps of an SM)
 constexpr int kStreamWarp = 18 << 10;    // its target where tokens are streamed (12 warps)
 
 // Shared memory of a warp, in this order: two stages of rows, two of the
-// tokens' bf16 rows and statistics, the dots unless they are the CTA's.
+// tokens' bf16 rows and statistics, the dots unless they are the CTA's, the
+// stages' barriers.
 template <int BITS, int LW, bool MULTI>
 struct Bwd : RowStage<BITS, LW, MULTI> {
     using R = RowStage<BITS, LW, MULTI>;
+    static constexpr bool BULK = LW == 32;
+    static constexpr int ROW = BULK ? BulkStage<BITS, MULTI>::ROW : R::ROW;
+    __host__ __device__ static int rows(int seg) { return BULK ? BulkStage<BITS, MULTI>::bytes(seg) : R::bytes(seg); }
     __host__ __device__ static int stats(int SL) { return (3 * SL * R::TW * 4 + 15) & ~15; }
     __host__ __device__ static int token(int SL, bool live) { return R::BF16 * (live ? 2 : 1) + stats(SL); }
     __host__ __device__ static int dots(int SL) { return MULTI ? 0 : (SL * R::TW * 4 + 15) & ~15; }
-    __host__ __device__ static int fixed(int SL, bool live) {
-        return 2 * token(SL, live) + dots(SL);
-    }
-    __host__ __device__ static int warp(int seg, int SL, bool live) {
-        return 2 * R::bytes(seg) + fixed(SL, live);
-    }
-    // of the CTA, behind the warps': dots in two buffers used in turn, <h, o>, the sources' addresses
+    __host__ __device__ static int fixed(int SL, bool live) { return 2 * token(SL, live) + dots(SL) + 16; }
+    __host__ __device__ static int warp(int seg, int SL, bool live) { return 2 * rows(seg) + fixed(SL, live); }
+    // of the CTA, behind the warps': dots in two buffers used in turn, <h, o>,
+    // the sources' addresses, the abort flag
     __host__ __device__ static int cta(int warps, int S, int SL) {
-        return (MULTI ? (2 * warps * (SL + 1) * 4 + 15) & ~15 : 0) + S * 8;
+        return (MULTI ? (2 * warps * (SL + 1) * 4 + 15) & ~15 : 0) + S * 8 + 16;
     }
 };
 
@@ -98,21 +101,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
     const int warp_bytes = G::warp(seg, SL, LIVE);
     unsigned char* mine = dyn + wid * warp_bytes;
     const uint32_t st0 = smem_u32(mine);
-    const int tok_at = 2 * G::bytes(seg), tok_bytes = G::token(SL, LIVE);
+    const int tok_at = 2 * G::rows(seg), tok_bytes = G::token(SL, LIVE);
     unsigned char* rest = dyn + warps * warp_bytes;
     float* red = MULTI ? reinterpret_cast<float*>(rest)
                        : reinterpret_cast<float*>(mine + tok_at + 2 * tok_bytes) + tw * SL;
     float* ho_red = red + 2 * warps * SL;  // MULTI
     if (MULTI) rest += (2 * warps * (SL + 1) * 4 + 15) & ~15;
     const unsigned char** rows = reinterpret_cast<const unsigned char**>(rest);
+    volatile int* abort = reinterpret_cast<volatile int*>(rest + ((a.S * 8 + 15) & ~15));
+    const uint32_t bar = st0 + tok_at + 2 * tok_bytes + G::dots(SL);  // of stage 0; 8 bytes on, of stage 1
     for (int s = threadIdx.x; s < a.S; s += blockDim.x) rows[s] = a.rows[s];
+    if (threadIdx.x == 0) *abort = 0;
+    BulkStage<BITS, MULTI> bulk;
+    if constexpr (G::BULK) {
+        bulk.init(a, rows, seg);
+        for (int i = lane * 16; i < tok_at + 2 * tok_bytes; i += 512) sts128(st0 + i, make_uint4(0u, 0u, 0u, 0u));
+        if (lane == 0) {
+            mbar_init(reinterpret_cast<uint64_t*>(mine + (bar - st0)), 1);
+            mbar_init(reinterpret_cast<uint64_t*>(mine + (bar - st0) + 8), 1);
+            mbar_fence_init();
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeros before the copies
+    }
     const bool has = c0 < a.D, key = has && c0 < a.ko + a.R && c0 + 32 > a.ko;
     const bool warp_key = __any_sync(0xffffffffu, key);
+    // Bulk copies leave codes and bf16 rows as they lie in memory.  8 bits: a
+    // thread's 32 bytes of codes are read as two halves, the second first where
+    // that keeps the lanes of a phase on different banks, and its channels are
+    // those halves in that order.
+    const int sw = G::BULK && BITS == 8 ? (lane >> 2) & 1 : 0;
+    const int half[2] = {c0 + 16 * sw, c0 + 16 * (1 - sw)};  // channels of pairs 0-7 and 8-15
+    auto chan = [&](int i) { return half[i / 8] + 2 * (i % 8); };  // of pair i
     f2 q[16], dq[16], dw[16];
-    uint32_t mask = 0;  // bit i: channel c0 + i is a key channel
+    uint32_t mask = 0;  // bits 2i, 2i + 1: the channels of pair i are in the key
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int j = c0 + 2 * i - a.ko;
+        const int j = chan(i) - a.ko;
         const bool x = j >= 0 && j < a.R, y = j + 1 >= 0 && j + 1 < a.R;
         q[i] = f2_make(x ? bf16_bits_to_float(__ldg(a.q + j)) : 0.0f, y ? bf16_bits_to_float(__ldg(a.q + j + 1)) : 0.0f);
         mask |= (x ? 1u : 0u) << (2 * i) | (y ? 1u : 0u) << (2 * i + 1);
@@ -121,33 +145,65 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
     const bool ragged = __any_sync(0xffffffffu, mask != 0xffffffffu);
     __syncthreads();
     uint32_t code_at[CH], scale_at;
-    G::places(seg, code_at, scale_at);
+    if constexpr (G::BULK) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) code_at[i] = lane * (16 * CH) + (CH == 2 ? (i ^ sw) * 16 : 0);
+        scale_at = seg * (512 * CH) + lane;
+    } else {
+        G::places(seg, code_at, scale_at);
+    }
+    // 8 channels of a token's bf16 row: pairs 4 i ff.
+    auto bf16_part = [&](uint32_t at, int i) {
+        if constexpr (G::BULK) return lds128(at + lane * 64 + (i ^ (2 * sw)) * 16);
+        else return G::bf16_part(at, i);
+    };
+    auto scale = [&](uint32_t base, int r) {
+        if constexpr (G::BULK) return cache_scale(lds8(base + scale_at + r * 32));
+        else return G::scale(base, scale_at, r);
+    };
     const float inv_D = 1.0f / static_cast<float>(a.D), inv_R = 1.0f / static_cast<float>(a.R);
 
     const int per = MULTI ? 1 : warps * TW;
     const long long stride = static_cast<long long>(gridDim.x) * per;
     const long long first = static_cast<long long>(blockIdx.x) * per + (MULTI ? 0 : wid * TW);
-    auto copy_rows = [&](int stage, long long n0, int g) {
-        G::copy(a, rows, st0 + stage * G::bytes(seg), seg, n0, g * seg, min(seg, a.S - g * seg));
-    };
-    auto copy_token = [&](int tb, long long n0) {
-        const uint32_t at = st0 + tok_at + tb * tok_bytes;
-        G::copy_bf16(b.dy, a.D, at, n0, a.N, a.D);
-        if constexpr (LIVE) G::copy_bf16(a.live, a.live_ld, at + G::BF16, n0, a.N, a.D);
-        const uint32_t st = at + G::BF16 * (LIVE ? 2 : 1);
-        for (int i = lane; i < TW * SL; i += 32) {
-            const long long from = TW == 1 ? n0 * SL + i : min(n0 + i / SL, a.N - 1) * SL + i % SL;
-            cp_async_4s(st + i * 4, a.alpha + from);
-            cp_async_4s(st + (TW * SL + i) * 4, a.rstd + from);
-            cp_async_4s(st + (2 * TW * SL + i) * 4, a.logit + from);
+    uint32_t phases = 0, inflight = 0;  // bit s: parity that stage s waits for next, and whether copies to it are on their way
+    // copies of a segment's rows and, with_token, of the token's other rows and statistics
+    auto copy = [&](int stage, int tb, long long n0, int g, bool with_token) {
+        const uint32_t tok = st0 + tok_at + tb * tok_bytes;
+        const int s0 = g * seg, cnt = min(seg, a.S - s0);
+        if constexpr (G::BULK) {
+            if (!*abort) {
+                const uint32_t b0 = bar + 8 * stage, base = st0 + stage * G::rows(seg);
+                if (lane == 0)
+                    mbar_expect(b0, cnt * bulk.row_bytes() + (with_token ? bulk.bf16_bytes * (LIVE ? 2 : 1) : 0));
+                __syncwarp();
+                for (int r = lane; r < cnt; r += 32) bulk.copy_row(a, base, n0, s0 + r, r, b0);
+                if (with_token && lane == 0) bulk.copy_bf16(b.dy + n0 * a.D, tok, b0);
+                if (LIVE && with_token && lane == 1) bulk.copy_bf16(a.live + n0 * a.live_ld, tok + G::BF16, b0);
+                inflight |= 1u << stage;
+            }
+        } else {
+            if (with_token) {
+                G::copy_bf16(b.dy, a.D, tok, n0, a.N, a.D);
+                if constexpr (LIVE) G::copy_bf16(a.live, a.live_ld, tok + G::BF16, n0, a.N, a.D);
+            }
+            G::copy(a, rows, st0 + stage * G::rows(seg), seg, n0, s0, cnt);
         }
+        if (with_token) {
+            const uint32_t st = tok + G::BF16 * (LIVE ? 2 : 1);
+            for (int i = lane; i < TW * SL; i += 32) {
+                const long long from = TW == 1 ? n0 * SL + i : min(n0 + i / SL, a.N - 1) * SL + i % SL;
+                cp_async_4s(st + i * 4, a.alpha + from);
+                cp_async_4s(st + (TW * SL + i) * 4, a.rstd + from);
+                cp_async_4s(st + (2 * TW * SL + i) * 4, a.logit + from);
+            }
+        }
+        cp_async_commit();
     };
     constexpr int kFirst = NORM ? 0 : 1;
     int stage = 0, tb = 0, flip = 0;
     if (first < a.N) {
-        copy_token(0, first);
-        copy_rows(0, first, 0);
-        cp_async_commit();
+        copy(0, 0, first, 0, true);
     }
     for (long long n0 = first; n0 < a.N; n0 += stride) {
         const bool valid = n0 + tw < a.N;
@@ -162,31 +218,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
         auto load_g = [&](uint32_t at) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 u = G::bf16_part(at, i);
+                const uint4 u = bf16_part(at, i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) g[4 * i + k] = f2_bf16(u4_get(u, k));
             }
         };
         // makes the rows of (pass, segment) ready and starts the copies of what comes next
         auto next = [&](int pass, int seg_i) {
-            if (resident) {
-                if (pass != kFirst) return;
-                if (more) {
-                    copy_token(tb ^ 1, n0 + stride);
-                    copy_rows(stage ^ 1, n0 + stride, 0);
-                }
-            } else if (seg_i < nseg - 1 || pass < 2) {
-                copy_rows(stage ^ 1, n0, seg_i < nseg - 1 ? seg_i + 1 : 0);
-            } else if (more) {
-                copy_token(tb ^ 1, n0 + stride);
-                copy_rows(stage ^ 1, n0 + stride, 0);
+            if (resident && pass != kFirst) return;
+            if (!resident && (seg_i < nseg - 1 || pass < 2))
+                copy(stage ^ 1, tb, n0, seg_i < nseg - 1 ? seg_i + 1 : 0, false);
+            else if (more)
+                copy(stage ^ 1, tb ^ 1, n0 + stride, 0, true);
+            else
+                cp_async_commit();
+            if constexpr (G::BULK) {
+                if (mbar_wait_s(bar + 8 * stage, phases >> stage & 1u, abort, &g_cached_bwd_error, kSiteCached))
+                    phases ^= 1u << stage, inflight &= ~(1u << stage);
             }
-            cp_async_commit();
             cp_async_wait<1>();
             __syncwarp();
         };
         auto done = [&](int pass, int seg_i) {
-            __syncwarp();
+            if (G::BULK && pass == 2) read_done(dq[15]);
+            else __syncwarp();
             if (!resident || pass == 2) stage ^= 1;
         };
         if constexpr (NORM) {
@@ -195,7 +250,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
             for (int i = 0; i < 16; ++i) o[i] = 0ull;
             for (int u = 0; u < nseg; ++u) {
                 next(0, u);
-                const uint32_t base = st0 + stage * G::bytes(seg);
+                const uint32_t base = st0 + stage * G::rows(seg);
                 const int s0 = u * seg, cnt = min(seg, a.S - s0);
                 auto mix = [&](auto count, int r0) {
                     constexpr int K = decltype(count)::value;
@@ -203,7 +258,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                     float c[K];
 #pragma unroll
                     for (int r = 0; r < K; ++r)
-                        w[r] = G::codes(base, code_at, r0 + r), c[r] = al[s0 + r0 + r] * G::scale(base, scale_at, r0 + r);
+                        w[r] = G::codes(base, code_at, r0 + r), c[r] = al[s0 + r0 + r] * scale(base, r0 + r);
 #pragma unroll
                     for (int r = 0; r < K; ++r) {
                         uint32_t h[16];
@@ -221,7 +276,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 const float c = al[a.S];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 x = G::bf16_part(tok + G::BF16, i);
+                    const uint4 x = bf16_part(tok + G::BF16, i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[4 * i + k] = f2_fma(f2_bf16(u4_get(x, k)), f2_dup(c), o[4 * i + k]);
                 }
@@ -232,7 +287,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
             if (has) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 w = c0 + 8 * i < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + c0) + i) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 w = chan(4 * i) < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + chan(4 * i))) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int j = 4 * i + k;
@@ -260,14 +315,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
         for (int u = 0; u < nseg; ++u) {
             next(1, u);
             if (!NORM && u == 0) load_g(tok);
-            const uint32_t base = st0 + stage * G::bytes(seg);
+            const uint32_t base = st0 + stage * G::rows(seg);
             const int s0 = u * seg, cnt = min(seg, a.S - s0);
             auto dots = [&](auto count, int r0) {
                 constexpr int K = decltype(count)::value;
                 CacheCodes<BITS> w[K];
                 float sc[K], p[K];
 #pragma unroll
-                for (int r = 0; r < K; ++r) w[r] = G::codes(base, code_at, r0 + r), sc[r] = G::scale(base, scale_at, r0 + r);
+                for (int r = 0; r < K; ++r) w[r] = G::codes(base, code_at, r0 + r), sc[r] = scale(base, r0 + r);
 #pragma unroll
                 for (int r = 0; r < K; ++r) {
                     uint32_t h[16];
@@ -292,7 +347,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
             f2 d = 0ull;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 x = G::bf16_part(tok + G::BF16, i);
+                const uint4 x = bf16_part(tok + G::BF16, i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) d = f2_fma(f2_bf16(u4_get(x, k)), g[4 * i + k], d);
             }
@@ -331,10 +386,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
         __syncwarp();
         for (int u = 0; u < nseg; ++u) {
             next(2, u);
-            const uint32_t base = st0 + stage * G::bytes(seg);
+            const uint32_t base = st0 + stage * G::rows(seg);
             const int s0 = u * seg, cnt = min(seg, a.S - s0);
             auto store = [&](int s, const uint32_t (&o)[16]) {
-                if (b.want_dsrc && valid) store_bf16x32(b.dsrc[s] + n * b.dsrc_ld + c0, a.D - c0, b.wide_src, o);
+                if (b.want_dsrc && valid) store_halves(b.dsrc[s] + n * b.dsrc_ld, half, a.D, b.wide_src, o);
             };
             // one row's gradient and its part of dq; RAGGED: some thread of the warp has channels outside the key
             auto grad = [&](auto ragged_c, int r) {
@@ -342,7 +397,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 const int s = s0 + r;
                 const f2 as = f2_dup(al[s]), x1 = f2_dup(k1[s]);
                 const CacheCodes<BITS> w = G::codes(base, code_at, r);
-                const float sc = RAGGED && !mask ? 0.0f : G::scale(base, scale_at, r);
+                const float sc = RAGGED && !mask ? 0.0f : scale(base, r);
                 const float y = valid ? k1[s] * sc : 0.0f, z = k2[s] * sc;
                 uint32_t h[16], o[16];
                 w.unpack(h);
@@ -374,7 +429,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 uint32_t o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    uint32_t u = u4_get(G::bf16_part(tok + G::BF16, i / 4), i % 4);
+                    uint32_t u = u4_get(bf16_part(tok + G::BF16, i / 4), i % 4);
                     if (!(mask >> (2 * i) & 1u)) u &= 0xffff0000u;
                     if (!(mask >> (2 * i + 1) & 1u)) u &= 0x0000ffffu;
                     const f2 v = f2_bf16(u);
@@ -383,31 +438,67 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                     d = f2_fma(q[i], f2_dup(x1), d);
                     o[i] = f2_to_bf16(f2_fma(v, f2_dup(y2), d));
                 }
-                if (b.dlive && valid) store_bf16x32(b.dlive + n * b.dlive_ld + c0, a.D - c0, b.wide_live, o);
+                if (b.dlive && valid) store_halves(b.dlive + n * b.dlive_ld, half, a.D, b.wide_live, o);
             }
             done(2, u);
         }
         tb ^= 1;
     }
     cp_async_wait<0>();
-    // one partial row per CTA: the teams' sums are added in team order
+    if constexpr (G::BULK) {  // a wait ran out: leave no copy of this warp's in flight
+        const uint64_t t0 = global_timer_ns();
+        for (int u = 0; u < 2; ++u)
+            while ((inflight >> u & 1u) && !mbar_test_sleep_s(bar + 8 * u, phases >> u & 1u, 20000u))
+                if (global_timer_ns() - t0 > kWaitLimitNs) break;
+    }
+    // One partial row per CTA.  Teams of less than the CTA are added in a fixed
+    // order: over the warp's teams by shuffles, over the warps in shared memory.
     const int W = a.R + (NORM ? a.D : 0);
     float* part = b.part + static_cast<size_t>(blockIdx.x) * W;
-    const int teams = MULTI ? 1 : warps * TW, team = MULTI ? 0 : wid * TW + tw;
-    for (int u = 0; u < teams; ++u) {
-        if (team == u && has) {
+    if constexpr (MULTI) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float x = i & 1 ? f2_get(dq[i / 2]).y : f2_get(dq[i / 2]).x;
-                const int j = c0 + i - a.ko;
-                if (mask >> i & 1u) part[j] = u ? part[j] + x : x;
-                if (NORM && c0 + i < a.D) {
-                    const float y = i & 1 ? f2_get(dw[i / 2]).y : f2_get(dw[i / 2]).x;
-                    part[a.R + c0 + i] = u ? part[a.R + c0 + i] + y : y;
+        for (int i = 0; i < 32; ++i) {
+            const float2 x = f2_get(dq[i / 2]), y = f2_get(dw[i / 2]);
+            const int j = chan(i / 2) + i % 2;
+            if (has && (mask >> i & 1u)) part[j - a.ko] = i % 2 ? x.y : x.x;
+            if (NORM && j < a.D) part[a.R + j] = i % 2 ? y.y : y.x;
+        }
+    } else {
+        float* sums = reinterpret_cast<float*>(dyn);  // [2][LW][33], over what the warps had
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float2 x2 = f2_get(dq[i / 2]), y2 = f2_get(dw[i / 2]);
+            float x = i % 2 ? x2.y : x2.x, y = i % 2 ? y2.y : y2.x;
+#pragma unroll
+            for (int o = LW; o < 32; o <<= 1) {
+                x += __shfl_xor_sync(0xffffffffu, x, o);
+                if constexpr (NORM) y += __shfl_xor_sync(0xffffffffu, y, o);
+            }
+            dq[i / 2] = i % 2 ? f2_make(f2_get(dq[i / 2]).x, x) : f2_make(x, x2.y);
+            dw[i / 2] = i % 2 ? f2_make(f2_get(dw[i / 2]).x, y) : f2_make(y, y2.y);
+        }
+        for (int u = 0; u < warps; ++u) {
+            if (wid == u && tw == 0) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float2 x = f2_get(dq[i / 2]), y = f2_get(dw[i / 2]);
+                    float* d0 = sums + l * 33 + i;
+                    float* d1 = d0 + LW * 33;
+                    *d0 = (u ? *d0 : 0.0f) + (i % 2 ? x.y : x.x);
+                    if (NORM) *d1 = (u ? *d1 : 0.0f) + (i % 2 ? y.y : y.x);
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
+        if (wid == 0 && tw == 0 && has) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int j = chan(i / 2) + i % 2;
+                if (mask >> i & 1u) part[j - a.ko] = sums[l * 33 + i];
+                if (NORM && j < a.D) part[a.R + j] = sums[LW * 33 + l * 33 + i];
+            }
+        }
     }
 }
 
@@ -444,6 +535,13 @@ auto by_team(int D, F f) {
 }
 
 }  // namespace
+
+unsigned take_cached_bwd_error() {
+    unsigned v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_cached_bwd_error, sizeof v) != cudaSuccess) return 0xffffffffu;
+    if (v) cudaMemcpyToSymbol(g_cached_bwd_error, &zero, sizeof zero);
+    return v;
+}
 
 int cached_bwd_grid(int S, bool live, long long N, int D, int bits, int sm_count) {
     auto f = [&](auto bb, auto lw, auto multi) {

@@ -80,31 +80,6 @@ WidePlan wide_plan(int D, int S, bool live, bool norm, int bits, int nc, int w, 
     return p;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// All lanes meet here, each after `v`, which must be computed from the last
-// shared-memory loads of what is then overwritten by a bulk copy: the vote
-// cannot issue while a load is in flight.
-__device__ __forceinline__ void read_done(f2 v) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.eq.u64 p, %0, 0x7fc12345;\n\tvote.sync.any.pred q, p, 0xffffffff;\n\t}" ::"l"(v) : "memory");
-    __syncwarp();
-}
-
 // The query's channels c0 .. c0 + 31 as halves times 2^sh, zero outside the
 // key.  sh puts the query's largest magnitude in [2^14, 2^15).  bf16 has fewer
 // significand bits than a half, so every channel down to 2^-28 of the largest
@@ -231,8 +206,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
         }
     };
     auto expect = [&](int cnt) {
-        if (lane == 0)
-            asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cnt * part_bytes) : "memory");
+        if (lane == 0) mbar_expect(bar, cnt * part_bytes);
         __syncwarp();
     };
     const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0;

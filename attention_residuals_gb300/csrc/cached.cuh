@@ -224,5 +224,6 @@ cudaError_t launch_cached_wide4(const CachedArgs& a, int sm_count, cudaStream_t 
 unsigned take_cached_wide8_error();
 unsigned take_cached_wide4_error();
 unsigned take_cached_fwd_error();
+unsigned take_cached_bwd_error();
 
 }  // namespace attnres

@@ -28,6 +28,36 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// Announce `bytes` to the barrier at shared address `bar` (one arrival).
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// All lanes meet here, each after `v`, which must be computed from the last
+// shared-memory loads of what is then overwritten by a bulk copy: the vote
+// cannot issue while a load is in flight.
+__device__ __forceinline__ void read_done(f2 v) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.eq.u64 p, %0, 0x7fc12345;\n\tvote.sync.any.pred q, p, 0xffffffff;\n\t}" ::"l"(v) : "memory");
+    __syncwarp();
+}
+
 template <int LW>
 __device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
@@ -160,6 +190,44 @@ struct RowStage {
     static __device__ __forceinline__ uint4 bf16_part(uint32_t base, int i) {
         const int c = (threadIdx.x & 31) * 4 + i;
         return lds128(base + (c ^ ((c >> 3) & 3)) * 16);
+    }
+};
+
+// The same parts of a warp's shared memory filled by bulk copies (teams of
+// whole warps): two copies a row instead of an instruction for every 16 bytes
+// of each lane.  Nothing is written behind a row's end: a stage starts as
+// zeros, so what a row does not have reads as zero.  Statistics are left out.
+template <int BITS, bool MULTI>
+struct BulkStage {
+    static constexpr int CH = BITS / 4;
+    static constexpr int ROW = 512 * CH + 32;  // a row's codes; its scales behind the codes of all rows
+    __host__ __device__ static int bytes(int seg) { return seg * ROW; }
+
+    const unsigned char* const* rows;
+    uint32_t code_from, code_bytes, scale_from, scale_bytes, bf16_from, bf16_bytes;  // of the warp, in a record and in a bf16 row
+    int seg;
+
+    __device__ __forceinline__ void init(const CachedArgs& a, const unsigned char* const* table, int rows_a_segment) {
+        const uint32_t w = MULTI ? threadIdx.x >> 5 : 0;
+        const uint32_t rec = (a.stat + 8 + 15) & ~15u;
+        rows = table;
+        seg = rows_a_segment;
+        code_from = w * 512 * CH;
+        code_bytes = min(a.codes - code_from, 512u * CH);
+        scale_from = a.codes + w * 32;
+        scale_bytes = min(rec - scale_from, 32u);
+        bf16_from = w * 1024;  // elements
+        bf16_bytes = min((a.D - bf16_from) * 2u, 2048u);
+    }
+    __device__ __forceinline__ uint32_t row_bytes() const { return code_bytes + scale_bytes; }
+    // by one lane
+    __device__ __forceinline__ void copy_row(const CachedArgs& a, uint32_t base, long long n, int s, int r, uint32_t bar) const {
+        const unsigned char* p = rows[s] + n * a.row_ld;
+        bulk_load(base + r * (512 * CH), p + code_from, code_bytes, bar);
+        bulk_load(base + seg * (512 * CH) + r * 32, p + scale_from, scale_bytes, bar);
+    }
+    __device__ __forceinline__ void copy_bf16(const uint16_t* x, uint32_t dst, uint32_t bar) const {
+        bulk_load(dst, x + bf16_from, bf16_bytes, bar);
     }
 };
 
