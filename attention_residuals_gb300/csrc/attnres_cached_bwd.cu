@@ -33,17 +33,17 @@ constexpr int kStreamWarp = 18 << 10;    // its target where tokens are streamed
 
 // Shared memory of a warp, in this order: two stages of rows, two of the
 // tokens' bf16 rows and statistics, the dots unless they are the CTA's, the
-// stages' barriers.
+// stages' barriers and (teams of whole warps) the output's weight.
 template <int BITS, int LW, bool MULTI>
 struct Bwd : RowStage<BITS, LW, MULTI> {
     using R = RowStage<BITS, LW, MULTI>;
     static constexpr bool BULK = LW == 32;
     static constexpr int ROW = BULK ? BulkStage<BITS, MULTI>::ROW : R::ROW;
     __host__ __device__ static int rows(int seg) { return BULK ? BulkStage<BITS, MULTI>::bytes(seg) : R::bytes(seg); }
-    __host__ __device__ static int stats(int SL) { return (3 * SL * R::TW * 4 + 15) & ~15; }
+    __host__ __device__ static int stats(int SL) { return ((3 * SL + 1) * R::TW * 4 + 15) & ~15; }
     __host__ __device__ static int token(int SL, bool live) { return R::BF16 * (live ? 2 : 1) + stats(SL); }
     __host__ __device__ static int dots(int SL) { return MULTI ? 0 : (SL * R::TW * 4 + 15) & ~15; }
-    __host__ __device__ static int fixed(int SL, bool live) { return 2 * token(SL, live) + dots(SL) + 16; }
+    __host__ __device__ static int fixed(int SL, bool live) { return 2 * token(SL, live) + dots(SL) + 16 + (BULK ? R::BF16 : 0); }
     __host__ __device__ static int warp(int seg, int SL, bool live) { return 2 * rows(seg) + fixed(SL, live); }
     // of the CTA, behind the warps': dots in two buffers used in turn, <h, o>,
     // the sources' addresses, the abort flag
@@ -161,6 +161,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
         if constexpr (G::BULK) return cache_scale(lds8(base + scale_at + r * 32));
         else return G::scale(base, scale_at, r);
     };
+    const uint32_t w_at = bar + 16 + lane * 16;  // [4][32] vectors, in the order of each lane's registers
+    if constexpr (G::BULK && NORM) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sts128(w_at + i * 512, chan(4 * i) < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + chan(4 * i))) : make_uint4(0u, 0u, 0u, 0u));
+        __syncwarp();
+    }
     const float inv_D = 1.0f / static_cast<float>(a.D), inv_R = 1.0f / static_cast<float>(a.R);
 
     const int per = MULTI ? 1 : warps * TW;
@@ -197,6 +204,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 cp_async_4s(st + (TW * SL + i) * 4, a.rstd + from);
                 cp_async_4s(st + (2 * TW * SL + i) * 4, a.logit + from);
             }
+            if (NORM && lane < TW) cp_async_4s(st + (3 * TW * SL + lane) * 4, a.o_rstd + min(n0 + lane, a.N - 1));
         }
         cp_async_commit();
     };
@@ -268,6 +276,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                     }
                 };
                 int r = 0;
+#pragma unroll 1
                 for (; r + 2 <= cnt; r += 2) mix(std::integral_constant<int, 2>{}, r);
                 if (r < cnt) mix(std::integral_constant<int, 1>{}, r);
                 done(0, u);
@@ -282,12 +291,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 }
             }
             load_g(tok);
-            const float r = a.o_rstd[n];
+            const float r = (al - tw * SL)[3 * TW * SL + tw];
             f2 s2 = 0ull;
             if (has) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 w = chan(4 * i) < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + chan(4 * i))) : make_uint4(0u, 0u, 0u, 0u);
+                    uint4 w;
+                    if constexpr (G::BULK) w = lds128(w_at + i * 512);
+                    else w = chan(4 * i) < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + chan(4 * i))) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int j = 4 * i + k;
@@ -338,9 +349,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 lanes_sum_to<LW>(p, out + s0 + r0);
             };
             int r = 0;
-            for (; r + 4 <= cnt; r += 4) dots(std::integral_constant<int, 4>{}, r);
-            if (cnt & 2) dots(std::integral_constant<int, 2>{}, r), r += 2;
-            if (cnt & 1) dots(std::integral_constant<int, 1>{}, r);
+#pragma unroll 1
+            for (; r + 2 <= cnt; r += 2) dots(std::integral_constant<int, 2>{}, r);
+            if (r < cnt) dots(std::integral_constant<int, 1>{}, r);
             done(1, u);
         }
         if constexpr (LIVE) {
@@ -391,13 +402,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
             auto store = [&](int s, const uint32_t (&o)[16]) {
                 if (b.want_dsrc && valid) store_halves(b.dsrc[s] + n * b.dsrc_ld, half, a.D, b.wide_src, o);
             };
+            CacheCodes<BITS> ahead;  // the next row's codes, on their way while a row is worked on
+            float ahead_sc = 0.0f;
+            if (warp_key) ahead = G::codes(base, code_at, 0), ahead_sc = scale(base, 0);
             // one row's gradient and its part of dq; RAGGED: some thread of the warp has channels outside the key
             auto grad = [&](auto ragged_c, int r) {
                 constexpr bool RAGGED = decltype(ragged_c)::value;
                 const int s = s0 + r;
                 const f2 as = f2_dup(al[s]), x1 = f2_dup(k1[s]);
-                const CacheCodes<BITS> w = G::codes(base, code_at, r);
-                const float sc = RAGGED && !mask ? 0.0f : scale(base, r);
+                const CacheCodes<BITS> w = ahead;
+                const float sc = RAGGED && !mask ? 0.0f : ahead_sc;
+                ahead = G::codes(base, code_at, min(r + 1, cnt - 1));
+                ahead_sc = scale(base, min(r + 1, cnt - 1));
                 const float y = valid ? k1[s] * sc : 0.0f, z = k2[s] * sc;
                 uint32_t h[16], o[16];
                 w.unpack(h);
@@ -420,8 +436,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                     store(s0 + r, o);
                 }
             } else if (ragged) {
+#pragma unroll 1
                 for (int r = 0; r < cnt; ++r) grad(std::true_type{}, r);
             } else {
+#pragma unroll 1
                 for (int r = 0; r < cnt; ++r) grad(std::false_type{}, r);
             }
             if (LIVE && u == nseg - 1) {
