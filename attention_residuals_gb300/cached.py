@@ -182,7 +182,8 @@ def attnres_cache_write(values: torch.Tensor, *, bits: int = 8, key_rank: Option
     size = attnres_cache_row_bytes(D, bits)
     R = D if key_rank is None else int(key_rank)
     shape = (*values.shape[:-1], size)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(shape, dtype=torch.uint8, device=dev)
     elif out.shape != shape:
         raise ValueError(f"out must be uint8 {list(shape)}")
@@ -190,7 +191,8 @@ def attnres_cache_write(values: torch.Tensor, *, bits: int = 8, key_rank: Option
     rows, _, row_ld, _ = _record_rows(out, size, writable=True)
     _call("attnres_cache_write", dev, stream, x, ld, N, D, int(bits), R,
           D - R if key_offset is None else int(key_offset), rows, row_ld)
-    torch.autograd.graph.increment_version(out)
+    if given and not out.is_inference():    # a read whose backward still needs the old records finds out
+        torch.autograd.graph.increment_version(out)
     return out
 
 

@@ -161,6 +161,11 @@ attnres_status attnres_cached_fwd(const attnres_cached_params* p, const void* q,
     if (!aligned(y, 16) || !aligned(q, 2) || !aligned(alpha, 4) || !aligned(rstd, 4) || !aligned(logit, 4))
         return ATTNRES_ERR_ALIGNMENT;
     if (p->out_norm && (!aligned(w_o, 16) || !aligned(o_rstd, 4))) return ATTNRES_ERR_ALIGNMENT;
+    // y is written while other tokens are still read
+    const size_t row = static_cast<size_t>(p->D) * 2, n_y = static_cast<size_t>(p->N) * row;
+    for (int s = 0; s < p->S; ++s)
+        if (overlap(y, n_y, p->rows[s], span(p->N, p->row_ld, cache_row_bytes(p->D, p->bits)))) return ATTNRES_ERR_INVALID_ARG;
+    if (p->live && overlap(y, n_y, p->live, span(p->N, p->live_ld * 2, row))) return ATTNRES_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (!sms) return ATTNRES_ERR_CUDA;
     CachedArgs a;

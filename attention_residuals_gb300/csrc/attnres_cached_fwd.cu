@@ -1,13 +1,18 @@
-// attnres_cached_fwd.cu -- the softmax read over compressed cache rows.
+// attnres_cached_fwd.cu -- the softmax read over compressed cache rows, and the
+// choice between its two kernels (the other one: attnres_cached_wide.cuh).
 //
 // A team of threads shares a token, one thread per 32 channels (one scale
-// group: a thread's codes have one scale).  Rows come in blocks of four: the
-// codes are decoded once into half pairs (exact), multiplied with the query
-// (also as halves, see load_query) into FP32 sums, the four dots are added
-// over the team, and the online softmax (running maximum and sum) takes the
-// block into the FP32 mixture while its half pairs are still in registers.
-// The key statistic of a cached row is read from its record; the live bf16
-// source, read last, gets its own.
+// group: a thread's codes have one scale).  The token's rows come in segments,
+// the next segment being copied to the warp's shared memory while one is read:
+//   1. dots: codes decoded to half pairs (exact) times the query's halves, FP32
+//      sums (fma.rn.f32.f16), added over the team
+//   2. the running softmax (maximum and sum), by the lanes of every warp
+//   3. mixture: codes decoded again, widened and added in FP32
+// Decoding twice is cheaper than holding a segment's values: they would take
+// four times the registers of the codes.  The key statistic of a cached row is
+// read from its record; the live bf16 source, read last, gets its own.  What
+// bounds it: with few tokens the chain of a segment's copy, dots, exchange and
+// softmax (7 us for up to 152 tokens of S=10 D=4096), else instruction issue.
 #include <cstdlib>
 #include <type_traits>
 
@@ -313,9 +318,16 @@ __global__ void __launch_bounds__(256, 2) cached_fwd_kernel(const CachedArgs a) 
     }
 }
 
-// Tokens from which rows of more than 512 channels go to the kernel with a
-// warp or two a token; fewer are finished sooner by more threads each.
-constexpr long long kWideTokens = 1;
+// Whether many tokens of wide rows go to the kernel with one to four warps a
+// token: it spends fewer instructions a token, but fills the card and pays its
+// set-up only over a few tokens a warp.  Measured (us, this kernel against
+// that one, S=10 but where noted, output norm, 8 bits / 4 bits):
+//   D=1024 (S=8)  N=7296   27 / 21 against 26 / 23: this one at any length
+//   D=2048        N=2432   24 / 19 against 18 / 16, N=1216 15 / 12 against 18 / 15
+//   D=4096        N=2432   44 / 31 against 43 / 29, N=608 16 / 13 against 20 / 18
+//   D=5120        N=7296  146 / 110 against 142 / 114
+//   D=8192 (S=64) N=1216  231 / 155 against 185 / 144, N=304 62 / 43 against 99 / 75
+bool many_tokens(int D, long long N) { return D > 1024 && N >= (D <= 4096 ? 2400 : D <= 6144 ? 8000 : 1200); }
 
 template <int BITS, int LW, bool MULTI>
 cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
@@ -363,8 +375,8 @@ unsigned take_cached_fwd_error() {
 
 cudaError_t launch_cached_fwd(const CachedArgs& a, int bits, int sm_count, cudaStream_t stream) {
     const char* form = std::getenv("ATTNRES_CACHED_FWD");  // "warp" or "cta": one form wherever it fits (tests)
-    const bool wide = form && form[0] == 'w' ? true : form && form[0] == 'c' ? false : a.N >= kWideTokens;
-    if (cached_team(a.D) >= 32 && wide)
+    const bool warp = form && form[0] == 'w' ? a.D > 1024 : form && form[0] == 'c' ? false : many_tokens(a.D, a.N);
+    if (warp)
         return bits == 8 ? launch_cached_wide8(a, sm_count, stream) : launch_cached_wide4(a, sm_count, stream);
     return bits == 8 ? launch_bits<8>(a, sm_count, stream) : launch_bits<4>(a, sm_count, stream);
 }

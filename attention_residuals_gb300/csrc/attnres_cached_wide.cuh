@@ -1,5 +1,6 @@
 // attnres_cached_wide.cuh -- the softmax read over many tokens of compressed
-// rows of more than 512 channels: one warp a token (two above 4096 channels).
+// rows of more than 1024 channels: one warp a token (up to four above 4096
+// channels).
 //
 // A lane owns up to four groups of 32 channels and keeps their FP32 mixture in
 // registers, so what a token costs besides its values (the sums over the warp,
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
     auto chan = [&](int c, int i) { return (w * 32 * NC + c * 32 + lane) * 32 + 16 * (i ^ sw); };
     {  // the largest magnitude of the query, as bf16 bits
         uint32_t m = 0;
+#pragma unroll 8
         for (int j = threadIdx.x; j < a.R; j += blockDim.x) m = max(m, static_cast<uint32_t>(__ldg(a.q + j)) & 0x7fffu);
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) reinterpret_cast<uint32_t*>(own + pl.coef_at)[0] = m;
@@ -148,25 +150,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
         top = max(top, *reinterpret_cast<const uint32_t*>(dyn + pl.warp_at + i * pl.warp_bytes + pl.coef_at));
     const int sh = min(141 - static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7), 114);
     const float back = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-    if (team == 0) {  // the query and the output's weight, in the order of each lane's registers
+    // the query and the output's weight, in the order of each lane's registers
+    for (int e = warp; e < NC * W; e += WARPS) {  // group e * 32 + lane
+        uint32_t q[16];
+        query_halves(a, (e * 32 + lane) * 32, sh, q);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            uint32_t q[16];
-            query_halves(a, (w * 32 * NC + c * 32 + lane) * 32, sh, q);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = 4 * (i ^ (2 * sw));
-                uint4 v;
-                v.x = k == 0 ? q[0] : k == 4 ? q[4] : k == 8 ? q[8] : q[12];
-                v.y = k == 0 ? q[1] : k == 4 ? q[5] : k == 8 ? q[9] : q[13];
-                v.z = k == 0 ? q[2] : k == 4 ? q[6] : k == 8 ? q[10] : q[14];
-                v.w = k == 0 ? q[3] : k == 4 ? q[7] : k == 8 ? q[11] : q[15];
-                sts128(sm + pl.q_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16, v);
-                if constexpr (NORM) {
-                    const int j = chan(c, i / 2) + 8 * (i & 1);
-                    sts128(sm + pl.w_at + (((w * NC + c) * 4 + i) * 32 + lane) * 16,
-                           j < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + j)) : make_uint4(0u, 0u, 0u, 0u));
-                }
+        for (int i = 0; i < 4; ++i) {
+            // 8 bits, halves swapped: quad i of the registers is quad i ^ 2 of the channels
+            const uint4 x = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+            sts128(sm + pl.q_at + ((e * 4 + (i ^ (2 * sw))) * 32 + lane) * 16, x);
+            if constexpr (NORM) {
+                const int j = (e * 32 + lane) * 32 + 8 * i;
+                sts128(sm + pl.w_at + ((e * 4 + (i ^ (2 * sw))) * 32 + lane) * 16,
+                       j < a.D ? __ldg(reinterpret_cast<const uint4*>(a.w_o + j)) : make_uint4(0u, 0u, 0u, 0u));
             }
         }
     }
@@ -489,7 +485,6 @@ cudaError_t launch_bits(const CachedArgs& a, int sm_count, cudaStream_t stream) 
     // 4 bits 318 us with <4, 1, 8> against 320 (2, 2, 16) and 351 (2, 2, 12),
     // 8 bits 387 against 401 and 432; S=64 N=8192 D=8192, 4 bits 904 with
     // <2, 4, 16> against 956 (4, 2, 8) and 941 (2, 4, 12).
-    if (groups <= 32) return launch_t<BITS, 1, 1, 20>(a, sm_count, stream);
     if (groups <= 64) return launch_t<BITS, 2, 1, 16>(a, sm_count, stream);
     if (groups <= 96) return launch_t<BITS, 3, 1, 12>(a, sm_count, stream);
     if (groups <= 128) return launch_t<BITS, 4, 1, 8>(a, sm_count, stream);

@@ -532,7 +532,11 @@ typedef struct {
 /*
  * The read of attnres_fwd with the records' values as sources.  Outputs:
  * y bf16 [N, D]; alpha, rstd, logit f32 [N, S (+ 1 with live)]; o_rstd f32
- * [N], required iff out_norm.  w_o starts on a 16-byte boundary.
+ * [N], required iff out_norm.  w_o starts on a 16-byte boundary; y must not
+ * overlap the records or the live source.
+ * Two kernels serve it: a CTA a token (rows of up to 1024 channels and fewer
+ * tokens), or one to four warps a token; ATTNRES_CACHED_FWD=cta or warp in the
+ * environment (read on every call) forces one where it can run.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA.
  */
 attnres_status attnres_cached_fwd(const attnres_cached_params* p, const void* q, const void* w_o, void* y, float* alpha,

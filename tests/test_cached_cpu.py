@@ -102,6 +102,8 @@ def test_pointer_and_overlap_refusals(lib):
     assert fwd(ctypes.byref(p), None, None, f, f, f, f, None, None) == 1
     assert fwd(ctypes.byref(p), f, None, f + 8, f, f, f, None, None) == 2
     assert fwd(ctypes.byref(p), f, None, f, f + 2, f, f, None, None) == 2
+    assert fwd(ctypes.byref(p), f, None, 0x210000 + 64, f, f, f, None, None) == 1   # y over a source's records
+    assert fwd(ctypes.byref(params(live=0xa00000)), f, None, 0xa00000 - 512, f, f, f, None, None) == 1
     n = params(norm=1)
     assert fwd(ctypes.byref(n), f, None, f, f, f, f, f, None) == 1           # no weight
     assert fwd(ctypes.byref(n), f, f, f, f, f, f, None, None) == 1           # no o_rstd

@@ -135,7 +135,12 @@ SHAPES = [
     (8, 2, 1024, 1024, 0, False, False, 1.0),
     (17, 9, 1032, 300, 732, False, True, 1.0),
     (10, 23, 2056, 520, 1001, True, False, 1.0),
+    (3, 31, 1056, 1056, 0, True, True, 1.0),
+    (10, 23, 2072, 700, 1300, True, True, 1.0),
+    (5, 1300, 2048, 512, 1536, False, True, 1.0),
     (4, 450, 4096, 1024, 2048, False, True, 1.0),
+    (11, 13, 5000, 5000, 0, True, True, 1.0),
+    (40, 7, 6152, 3000, 3000, False, True, 1.0),
     (12, 11, 4104, 4104, 0, True, True, 1.0),
     (33, 6, 8192, 2048, 6144, True, True, 1.0),
     (127, 2, 512, 512, 0, True, True, 1.0),
@@ -144,9 +149,13 @@ SHAPES = [
 ]
 
 
+@pytest.mark.parametrize("form", ["cta", "warp"])  # the read's two kernels; rows of up to 1024 channels have one
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("S,N,D,R,ko,live,norm,scale", SHAPES)
-def test_read_and_gradient(S, N, D, R, ko, live, norm, scale, bits):
+def test_read_and_gradient(S, N, D, R, ko, live, norm, scale, bits, form, monkeypatch):
+    if form == "warp" and D <= 1024:
+        pytest.skip("one kernel")
+    monkeypatch.setenv("ATTNRES_CACHED_FWD", form)
     x, rows, v = sources(S, N, D, bits, R, ko, seed=S * 7 + D)
     lv = rand((N, D), 11) if live else None
     q = rand((R,), 12, R ** -0.5)
@@ -429,3 +438,63 @@ def test_gradient_against_differences(bits):
             slope = (call(up) - call(down)) / (2 * h)
             # h^2 / 6 times a third derivative; these are of order 10 for inputs of order 1
             assert abs(got[i] - slope) <= bound[i] + 20 * h * h + 1e-9
+
+
+def test_inference_mode():
+    """Serving: a cache made and filled under inference mode, and read from outside it."""
+    with torch.inference_mode():
+        cache = torch.empty((2, 4, attnres_cache_row_bytes(64, 4)), dtype=torch.uint8, device="cuda")
+        for s in range(2):
+            attnres_cache_write(rand((4, 64), s), bits=4, out=cache[s])
+        q = rand((64,), 5)
+        a = attnres_cached(cache, q, 64, bits=4)
+        b = attnres_cached_fwd(cache, q, 64, bits=4)["y"]
+    attnres_cache_write(rand((4, 64), 1), bits=4, out=cache[1])
+    c = attnres_cached_fwd(cache, q, 64, bits=4)["y"]
+    assert torch.equal(a, b) and torch.equal(b, c)
+
+
+@pytest.mark.parametrize("form", ["cta", "warp"])
+@pytest.mark.parametrize("bits,D", [(8, 200), (4, 200), (8, 2072), (4, 4096)])
+def test_forward_stores_stay_inside(bits, D, form, monkeypatch):
+    """Every output of the read between sentinel values, written whole; rows of a longer buffer behind the last
+    token stay as they are."""
+    monkeypatch.setenv("ATTNRES_CACHED_FWD", form)
+    S, N = 3, 21
+    _, rows, _ = sources(S, N, D, bits, D, 0)
+    q, w, lv = rand((D,), 1, D ** -0.5), rand((D,), 2), rand((N, D), 3)
+    how = dict(bits=bits, live=lv, w_o=w)
+    plain = attnres_cached_fwd(rows, q, D, **how)
+    bufs = {k: torch.full((N + 6,) + v.shape[1:], -7.0, dtype=v.dtype, device="cuda") for k, v in plain.items()}
+    got = attnres_cached_fwd(rows, q, D, out={k: v[2:2 + N] for k, v in bufs.items()}, **how)
+    for k, v in plain.items():
+        assert torch.equal(got[k], v) and got[k].data_ptr() == bufs[k][2:].data_ptr()
+        assert (bufs[k][:2] == -7).all() and (bufs[k][2 + N:] == -7).all(), k
+
+
+@pytest.mark.parametrize("form", ["cta", "warp"])
+def test_offsets_beyond_32_bits(form, monkeypatch):
+    """A source of more than 4 GB of records: the last tokens are read, and their gradients written, like any."""
+    monkeypatch.setenv("ATTNRES_CACHED_FWD", form)   # the same sums in the same order, whatever the length
+    D, N, bits, tail = 4096, 1_100_000, 8, 5
+    size = attnres_cache_row_bytes(D, bits)
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GB")
+    first, last = rand((1, D), 1), rand((tail, D), 2)
+    rows = torch.empty((1, N, size), dtype=torch.uint8, device="cuda")
+    assert rows.numel() > 1 << 32
+    rows[0] = attnres_cache_write(first, bits=bits)
+    attnres_cache_write(last, bits=bits, out=rows[0, N - tail:])
+    q = rand((D,), 3, D ** -0.5)
+    f = attnres_cached_fwd(rows, q, D, bits=bits)
+    small = attnres_cached_fwd(rows[:, N - tail:].clone(), q, D, bits=bits)
+    assert torch.equal(f["y"][N - tail:], small["y"]) and torch.equal(f["logit"][N - tail:], small["logit"])
+    assert torch.equal(f["y"][:2], attnres_cache_load(rows[0, :2], D, bits=bits))     # one source: its values
+    dy = f["y"]
+    g = attnres_cached_bwd(rows, q, dy, f, D, bits=bits)
+    gs = attnres_cached_bwd(rows[:, N - tail:].clone(), q, small["y"], small, D, bits=bits)
+    assert torch.equal(g["dvalues"][:, N - tail:], gs["dvalues"])
+    del g
+    back = attnres_cache_load(rows[0], D, bits=bits)
+    assert torch.equal(back[N - tail:], attnres_cache_load(attnres_cache_write(last, bits=bits), D, bits=bits))
+    assert torch.equal(attnres_cache_write(back, bits=bits)[N - tail:], rows[0, N - tail:])   # exact values write as they were
