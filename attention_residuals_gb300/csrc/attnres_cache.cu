@@ -73,23 +73,25 @@ __device__ __forceinline__ uint32_t quantise8(const CacheRowsArgs& a, unsigned c
     }
     if (c < a.ko + a.R && c + 8 > a.ko) {
         float g0 = 0.0f, g1 = 0.0f;
+        if (c < a.ko || c + 8 > a.ko + a.R) {  // the key begins or ends among the lane's channels
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = c + 2 * i - a.ko;
-            uint32_t hm = h[i];
-            if (j < 0 || j >= a.R) hm &= 0xffff0000u;
-            if (j + 1 < 0 || j + 1 >= a.R) hm &= 0x0000ffffu;
-            half2_dot(hm, hm, g0, g1);
+            for (int i = 0; i < 4; ++i) {
+                const int j = c + 2 * i - a.ko;
+                if (j < 0 || j >= a.R) h[i] &= 0xffff0000u;
+                if (j + 1 < 0 || j + 1 >= a.R) h[i] &= 0x0000ffffu;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) half2_dot(h[i], h[i], g0, g1);
         sq += finite ? (g0 + g1) * up * up : __uint_as_float(0x7fc00000u);
     }
     return finite ? static_cast<uint32_t>(k + 127) : 255u;
 }
 
-// A warp (JOIN false) or a CTA (JOIN) writes a row: blocks of 1024 channels, 8
-// a lane in each of four loads that are in flight together, four lanes a
-// group.  The 32 scales of a block are stored by one instruction.
-template <int BITS, bool JOIN>
+// A warp (JOIN false) or a CTA (JOIN) writes a row: blocks of 256 U channels, 8
+// a lane in each of U loads that are in flight together, four lanes a group.
+// The scales of a block are stored by one instruction.
+template <int BITS, int U, bool JOIN>
 __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(const CacheRowsArgs a) {
     __shared__ float part[kRowWarps];
     pdl_wait();
@@ -101,28 +103,28 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(const Cache
         const uint16_t* x = a.x + n * a.x_ld;
         unsigned char* row = a.rows + n * a.row_ld;
         float sq = 0.0f;
-        for (int base = JOIN ? wid * 1024 : 0; base < padded; base += JOIN ? kRowWarps * 1024 : 1024) {
-            uint4 v[4];
-            uint32_t k[4];
+        for (int base = JOIN ? wid * 256 * U : 0; base < padded; base += JOIN ? kRowWarps * 256 * U : 256 * U) {
+            uint4 v[U];
+            uint32_t k[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int c = base + 256 * u + lane * 8;
                 v[u] = c < a.D ? ld_global_nc_v4(x + c) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int c = base + 256 * u + lane * 8;
                 k[u] = quantise8<BITS>(a, row, c, c < padded, v[u], sq);
             }
             // lane l stores the scale of the block's group l: load l / 8, lanes 4 (l % 8) ff.
             uint32_t mine = 0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const uint32_t from = __shfl_sync(0xffffffffu, k[u], (lane & 7) * 4);
                 if (lane >> 3 == u) mine = from;
             }
             const uint32_t g = static_cast<uint32_t>(base) / 32 + lane;
-            if (g < groups) row[a.codes + g] = static_cast<uint8_t>(mine);
+            if (lane < 8 * U && g < groups) row[a.codes + g] = static_cast<uint8_t>(mine);
         }
         sq = warp_sum(sq);
         if constexpr (JOIN) {
@@ -202,9 +204,11 @@ cudaError_t launch_cache_write(const CacheRowsArgs& a, int bits, int sm_count, c
     // Few wide rows: a CTA a row, so that a row's loads are all in flight at
     // once.  More rows than warps on the card have enough in flight.
     const bool join = a.D > 1024 && a.N <= static_cast<long long>(sm_count) * 4;
-    const int grid = grid_for(join ? a.N : (a.N + kRowWarps - 1) / kRowWarps, sm_count * 12);
-    auto kern = bits == 8 ? (join ? cache_write_kernel<8, true> : cache_write_kernel<8, false>)
-                          : (join ? cache_write_kernel<4, true> : cache_write_kernel<4, false>);
+    const int grid = grid_for(join ? a.N : (a.N + kRowWarps - 1) / kRowWarps, sm_count * 16);
+    auto kern = bits == 8 ? (join ? cache_write_kernel<8, 4, true> : a.D <= 256 ? cache_write_kernel<8, 1, false>
+                                  : a.D <= 512 ? cache_write_kernel<8, 2, false> : cache_write_kernel<8, 4, false>)
+                          : (join ? cache_write_kernel<4, 4, true> : a.D <= 256 ? cache_write_kernel<4, 1, false>
+                                  : a.D <= 512 ? cache_write_kernel<4, 2, false> : cache_write_kernel<4, 4, false>);
     return launch_pdl(kern, dim3(grid), dim3(kRowWarps * 32), 0, stream, a);
 }
 

@@ -402,21 +402,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
             auto store = [&](int s, const uint32_t (&o)[16]) {
                 if (b.want_dsrc && valid) store_halves(b.dsrc[s] + n * b.dsrc_ld, half, a.D, b.wide_src, o);
             };
-            CacheCodes<BITS> ahead;  // the next row's codes, on their way while a row is worked on
-            float ahead_sc = 0.0f;
-            if (warp_key) ahead = G::codes(base, code_at, 0), ahead_sc = scale(base, 0);
             // one row's gradient and its part of dq; RAGGED: some thread of the warp has channels outside the key
-            auto grad = [&](auto ragged_c, int r) {
+            auto grad = [&](auto ragged_c, int r, uint32_t (&h)[16], float row_scale) {
                 constexpr bool RAGGED = decltype(ragged_c)::value;
                 const int s = s0 + r;
                 const f2 as = f2_dup(al[s]), x1 = f2_dup(k1[s]);
-                const CacheCodes<BITS> w = ahead;
-                const float sc = RAGGED && !mask ? 0.0f : ahead_sc;
-                ahead = G::codes(base, code_at, min(r + 1, cnt - 1));
-                ahead_sc = scale(base, min(r + 1, cnt - 1));
+                const float sc = RAGGED && !mask ? 0.0f : row_scale;
                 const float y = valid ? k1[s] * sc : 0.0f, z = k2[s] * sc;
-                uint32_t h[16], o[16];
-                w.unpack(h);
+                uint32_t o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if constexpr (RAGGED)
@@ -427,6 +420,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                 }
                 store(s, o);
             };
+            // two rows in turn: one is decoded while the other is worked on
+            auto grads = [&](auto ragged_c) {
+                uint32_t h0[16], h1[16];
+                float sc0, sc1 = 0.0f;
+                G::codes(base, code_at, 0).unpack(h0);
+                sc0 = scale(base, 0);
+#pragma unroll 1
+                for (int r = 0; r < cnt; r += 2) {
+                    const int r1 = min(r + 1, cnt - 1), r2 = min(r + 2, cnt - 1);
+                    G::codes(base, code_at, r1).unpack(h1);
+                    sc1 = scale(base, r1);
+                    grad(ragged_c, r, h0, sc0);
+                    if (r + 1 >= cnt) break;
+                    G::codes(base, code_at, r2).unpack(h0);
+                    sc0 = scale(base, r2);
+                    grad(ragged_c, r + 1, h1, sc1);
+                }
+            };
             if (!warp_key) {
                 for (int r = 0; r < cnt; ++r) {
                     const f2 as = f2_dup(al[s0 + r]);
@@ -436,11 +447,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
                     store(s0 + r, o);
                 }
             } else if (ragged) {
-#pragma unroll 1
-                for (int r = 0; r < cnt; ++r) grad(std::true_type{}, r);
+                grads(std::true_type{});
             } else {
-#pragma unroll 1
-                for (int r = 0; r < cnt; ++r) grad(std::false_type{}, r);
+                grads(std::false_type{});
             }
             if (LIVE && u == nseg - 1) {
                 const float as = al[a.S], x1 = k1[a.S], y1 = valid ? x1 : 0.0f, y2 = k2[a.S];
