@@ -35,7 +35,7 @@ struct WidePlan {
     uint32_t codes, scales;   // of a slot: bytes of codes, where the scales begin
     uint32_t stat;            // where the statistic is in a slot
     uint32_t q_at, w_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
-    uint32_t red_at, coef_at, z_at, bar_at;                         // in a warp's
+    uint32_t red_at, coef_at, z_at, bar_at, live_at;                // in a warp's
     size_t smem;
 };
 
@@ -64,7 +64,8 @@ WidePlan wide_plan(int D, int S, bool live, bool norm, int bits, int nc, int w, 
     p.abort_at = take(32);  // and the query's factor
     p.warp_at = off;
     off = 0;
-    p.bar_at = take(16);
+    p.bar_at = take(16);  // of the rows and of the live row
+    p.live_at = take(live ? nc * 2048 : 0);
     p.z_at = take(2 * SL * 4);
     p.red_at = take(2 * 32 * 4);
     p.coef_at = take(32 * 4);
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
     float* coef = reinterpret_cast<float*>(own + pl.coef_at);
     if (threadIdx.x == 0) *abort = 0;
     if (lane == 0) {
-        mbar_init(reinterpret_cast<uint64_t*>(own + pl.bar_at), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(reinterpret_cast<uint64_t*>(own + pl.bar_at + 8 * i), 1);
         mbar_fence_init();
     }
     for (int s = threadIdx.x; s < a.S; s += blockDim.x) rows[s] = a.rows[s];
@@ -205,6 +206,13 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
         if (lane == 0) mbar_expect(bar, cnt * part_bytes);
         __syncwarp();
     };
+    const uint32_t live_bytes = min((a.D - w * 1024 * NC) * 2u, 2048u * NC);
+    auto fetch_live = [&](long long n) {
+        if (lane == 0) {
+            mbar_expect(bar + 8, live_bytes);
+            bulk_load(smem_u32(own) + pl.live_at, a.live + n * a.live_ld + w * 1024 * NC, live_bytes, bar + 8);
+        }
+    };
     const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0;
     const float inv_D = 1.0f / static_cast<float>(a.D), inv_R = 1.0f / static_cast<float>(a.R);
     int flip = 0;
@@ -223,29 +231,38 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
     };
 
     const long long first = static_cast<long long>(blockIdx.x) * TEAMS + team, stride = static_cast<long long>(gridDim.x) * TEAMS;
-    uint32_t phase = 0, stuck_phase = 0;
-    bool stuck = false;  // a wait ran out (here or in another warp of the CTA): nothing more is fetched
+    uint32_t phases = 0;  // bit i: the parity barrier i is waited for next
+    uint32_t stuck = 0, stuck_phases = 0;  // waits that ran out (here or in another warp): nothing more is fetched
+    auto wait = [&](int i) {
+        if (!mbar_wait_s(bar + 8 * i, phases >> i & 1u, abort, &g_cached_wide_error, kSiteCached) && !(stuck >> i & 1u))
+            stuck |= 1u << i, stuck_phases |= (phases >> i & 1u) << i;
+        phases ^= 1u << i;
+    };
     if (first < a.N) {
         const int cnt = min(seg, a.S);
         expect(cnt);
         if (lane < cnt) fetch(first, lane, lane);
+        if constexpr (LIVE) fetch_live(first);
     }
     for (long long n = first; n < a.N; n += stride) {
         f2 acc[NC][16];
         float mx, sum;
         if constexpr (LIVE) {  // the live source first: it is the mixture, with weight 1
             float p0 = 0.0f, p1 = 0.0f;
-            const uint16_t* x = a.live + n * a.live_ld;
+            wait(1);
+            const uint32_t x = smem_u32(own) + pl.live_at - w * 2048 * NC;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = chan(c, i / 2) + 8 * (i & 1);
-                    const uint4 u = j < a.D ? ld_global_nc_v4(x + j) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 u = j < a.D ? lds128(x + j * 2) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[c][4 * i + k] = f2_bf16(u4_get(u, k));
                 }
             }
+            read_done(acc[NC - 1][15]);
+            if (n + stride < a.N && !*abort) fetch_live(n + stride);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 if (!(any_keys >> c & 1u)) continue;
@@ -289,9 +306,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
             }
         }
         for (int g = 0; g < nseg; ++g) {
-            if (!mbar_wait_s(bar, phase, abort, &g_cached_wide_error, kSiteCached) && !stuck) stuck = true, stuck_phase = phase;
-            phase ^= 1u;
             const int s0 = g * seg, cnt = min(seg, a.S - s0);
+            wait(0);
             // what the slots take next
             const bool last = g == nseg - 1;
             const long long nn = last ? n + stride : n;
@@ -337,12 +353,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
                     lanes_sum_to<32>(p, dotbuf + r0);
                 };
                 int r = 0;
-                if constexpr (K == 4) {
-                    for (; r + 4 <= cnt; r += 4) dots(std::integral_constant<int, 4>{}, r);
-                    if (r + 2 <= cnt) dots(std::integral_constant<int, 2>{}, r), r += 2;
-                } else {
-                    for (; r + 2 <= cnt; r += 2) dots(std::integral_constant<int, 2>{}, r);
-                }
+#pragma unroll 1
+                for (; r + K <= cnt; r += K) dots(std::integral_constant<int, K>{}, r);
+                if (K == 4 && r + 2 <= cnt) dots(std::integral_constant<int, 2>{}, r), r += 2;
                 if (r < cnt) dots(std::integral_constant<int, 1>{}, r);
             } else {
                 dotbuf[lane] = 0.0f;
@@ -455,8 +468,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
     }
     if (stuck) {  // leave no copy of this warp's in flight
         const uint64_t t0 = global_timer_ns();
-        while (!mbar_test_sleep_s(bar, stuck_phase, 20000u))
-            if (global_timer_ns() - t0 > kWaitLimitNs) break;
+        for (int i = 0; i < 2; ++i)
+            while ((stuck >> i & 1u) && !mbar_test_sleep_s(bar + 8 * i, stuck_phases >> i & 1u, 20000u))
+                if (global_timer_ns() - t0 > kWaitLimitNs) break;
     }
 }
 
