@@ -8,6 +8,14 @@
 // bf16 bits of the group's largest magnitude (integer maximum: a NaN or an
 // infinity is the largest of all).  The mean square of the key channels'
 // decoded values is summed in FP32 in a fixed order.
+//
+// A lane takes 8 channels a load (16 bytes), so the group's maximum is two
+// shuffles.  What bounds the write: instructions and HBM together.  81920 rows
+// of D=4096 under counters: 171 us in 8 bits (5.9 TB/s, 0.68 of the issue
+// slots), 156 us in 4 (5.4 TB/s, 0.74).
+//
+// Load: v = code * 2^k, exact in bf16; 16 channels a lane.  HBM bounds it: nine
+// sources of 8192 x 4096 from 4 bits in 119 us, 0.95 of the copy rate.
 #include "cached.cuh"
 #include "kernels.cuh"
 #include "launch_pdl.cuh"

@@ -13,7 +13,13 @@
 //   3. mixture: codes decoded again, widened and added in FP32; a slot that
 //      has been read takes the next segment's record at once.
 // What bounds it: instruction issue.  Decoding costs half an instruction a
-// value, the dot one, widening one, the packed FMA a half.
+// value and pass, the dot one, widening one, the packed FMA a half; at eight
+// warps an SM (the mixture fills the registers) half of the slots issue.
+// S=10 N=32768 D=4096 with the output norm: 294 us in 4 bits (3.4 TB/s), 359
+// us in 8 (4.6 TB/s); 8 blocks and a live row, N=16384, R=1024, 8 bits: 144 us
+// (5.7 TB/s).  Twelve warps with spills took 383 us for 318, two warps of two
+// groups a token 320, a barrier of its own for a segment's first rows 300 for
+// 294.
 #pragma once
 
 #include <type_traits>
@@ -495,9 +501,10 @@ template <int BITS>
 cudaError_t launch_bits(const CachedArgs& a, int sm_count, cudaStream_t stream) {
     const int groups = (a.D + 31) / 32;
     // groups a lane, warps a token, warps of an SM (as many as the registers
-    // allow without spilling).  Measured, output norm: S=10 N=32768 D=4096,
-    // 4 bits 318 us with <4, 1, 8> against 320 (2, 2, 16) and 351 (2, 2, 12),
-    // 8 bits 387 against 401 and 432; S=64 N=8192 D=8192, 4 bits 904 with
+    // allow without spilling).  Measured while the first of each took so long
+    // (slots refilled a segment at a time), output norm: S=10 N=32768 D=4096, 4
+    // bits 318 us with <4, 1, 8> against 320 (2, 2, 16) and 351 (2, 2, 12), 8
+    // bits 387 against 401 and 432; S=64 N=8192 D=8192, 4 bits 904 with
     // <2, 4, 16> against 956 (4, 2, 8) and 941 (2, 4, 12).
     if (groups <= 64) return launch_t<BITS, 2, 1, 16>(a, sm_count, stream);
     if (groups <= 96) return launch_t<BITS, 3, 1, 12>(a, sm_count, stream);
