@@ -6,7 +6,8 @@ attnres_cached_bwd are the read and its gradient over cached sources, and
 attnres_cached is the autograd operator.  Records are uint8 tensors
 [..., attnres_cache_row_bytes(D, bits)]; S of them (packed [S, ..., bytes], or
 a list) are the sources of a read.  As in ops.py, only pointers and sizes are
-marshalled here and CPU tensors are rejected.
+marshalled here and CPU tensors are rejected.  A call runs on the current
+stream of its tensors' device, or on `stream` as if that one were current.
 """
 from __future__ import annotations
 
@@ -31,15 +32,12 @@ def attnres_cache_row_bytes(D: int, bits: int) -> int:
     return n
 
 
-def _call(name: str, device, stream, *args) -> None:
-    """The library's function `name` with `args` and the stream (by default the
-    current one of the tensors' device), that device current."""
+def _call(name: str, device, *args) -> None:
+    """The library's function `name` with `args` and the current stream of the
+    tensors' device, that device current."""
     f = getattr(_lib.load(), name)
     index = device.index
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if index == torch.cuda.current_device():
         rc = f(*args, stream)
     else:
@@ -47,6 +45,22 @@ def _call(name: str, device, stream, *args) -> None:
             rc = f(*args, stream)
     if rc:
         _lib.check(rc, name)
+
+
+def _on(stream, rows: Records):
+    """Makes `stream` current: what a call allocates and the copies it makes of
+    inputs that it cannot address belong to the stream that it runs on."""
+    if not isinstance(rows, torch.Tensor) and not len(rows):
+        raise ValueError("need at least one cached source")
+    t = rows if isinstance(rows, torch.Tensor) else rows[0]
+    if not t.is_cuda:
+        raise TypeError("needs CUDA tensors")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device) if stream else \
+            torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError("stream must be on the tensors' device")
+    return torch.cuda.stream(stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -177,6 +191,9 @@ def attnres_cache_write(values: torch.Tensor, *, bits: int = 8, key_rank: Option
         D = values.shape[-1]
         R = D if key_rank is None else key_rank
         return cache_write(values, bits, R, D - R if key_offset is None else key_offset)
+    if stream is not None:
+        with _on(stream, values):
+            return attnres_cache_write(values, bits=bits, key_rank=key_rank, key_offset=key_offset, out=out)
     x, N, ld, keep = _bf16_rows(values, "values")
     D, dev = values.shape[-1], values.device
     size = attnres_cache_row_bytes(D, bits)
@@ -189,7 +206,7 @@ def attnres_cache_write(values: torch.Tensor, *, bits: int = 8, key_rank: Option
         raise ValueError(f"out must be uint8 {list(shape)}")
     _same_device(dev, out=out)
     rows, _, row_ld, _ = _record_rows(out, size, writable=True)
-    _call("attnres_cache_write", dev, stream, x, ld, N, D, int(bits), R,
+    _call("attnres_cache_write", dev, x, ld, N, D, int(bits), R,
           D - R if key_offset is None else int(key_offset), rows, row_ld)
     if given and not out.is_inference():    # a read whose backward still needs the old records finds out
         torch.autograd.graph.increment_version(out)
@@ -202,6 +219,9 @@ def attnres_cache_load(rows: torch.Tensor, D: int, *, bits: int = 8, out: Option
     if torch.compiler.is_compiling() and out is None and stream is None:
         from .custom_ops import cache_load
         return cache_load(rows, D, bits)
+    if stream is not None:
+        with _on(stream, rows):
+            return attnres_cache_load(rows, D, bits=bits, out=out)
     size = attnres_cache_row_bytes(D, bits)
     src, N, row_ld, keep = _record_rows(rows, size)
     shape, dev = (*rows.shape[:-1], D), rows.device
@@ -216,7 +236,7 @@ def attnres_cache_load(rows: torch.Tensor, D: int, *, bits: int = 8, out: Option
         dst, ld = r.data_ptr(), r.stride(0) if N > 1 else D
         if dst % 16 or ld % 8 or ld < D:
             raise ValueError("out: rows must start on 16-byte boundaries and not overlap")
-    _call("attnres_cache_load", dev, stream, src, row_ld, N, D, int(bits), dst, ld)
+    _call("attnres_cache_load", dev, src, row_ld, N, D, int(bits), dst, ld)
     return out
 
 
@@ -226,6 +246,10 @@ def attnres_cached_fwd(rows: Records, q: torch.Tensor, D: int, *, bits: int = 8,
     """The read over cached sources and, last, an optional bf16 source `live`
     [..., D].  Returns y [..., D] and the statistics alpha/rstd/logit
     [N, sources] and, with w_o, o_rstd [N].  `out` may supply tensors."""
+    if stream is not None:
+        with _on(stream, rows):
+            return attnres_cached_fwd(rows, q, D, bits=bits, live=live, w_o=w_o, eps=eps, scale=scale,
+                                      key_offset=key_offset, out=out)
     D = int(D)
     src = _Sources(rows, attnres_cache_row_bytes(D, bits))
     dev, N, S = src.device, src.N, len(src.addrs) + (live is not None)
@@ -253,7 +277,7 @@ def attnres_cached_fwd(rows: Records, q: torch.Tensor, D: int, *, bits: int = 8,
     logit = torch.empty((N, S), dtype=f32, device=dev) if logit is None else logit
     if w_o is not None and o_rstd is None:
         o_rstd = torch.empty((N,), dtype=f32, device=dev)
-    _call("attnres_cached_fwd", dev, stream, ctypes.byref(p), q.data_ptr(), _addr(w_o), y.data_ptr(), alpha.data_ptr(),
+    _call("attnres_cached_fwd", dev, ctypes.byref(p), q.data_ptr(), _addr(w_o), y.data_ptr(), alpha.data_ptr(),
           rstd.data_ptr(), logit.data_ptr(), _addr(o_rstd))
     return {"y": y, "alpha": alpha, "rstd": rstd, "logit": logit, "o_rstd": o_rstd}
 
@@ -275,6 +299,11 @@ def attnres_cached_bwd(rows: Records, q: torch.Tensor, dy: torch.Tensor, saved: 
     of the values that the codes stand for, which passed straight through is
     that of the rows written; None without need_dvalues), d_live, and dq/dw_o
     in bf16 and fp32.  `dvalues` and `workspace` may be given."""
+    if stream is not None:
+        with _on(stream, rows):
+            return attnres_cached_bwd(rows, q, dy, saved, D, bits=bits, live=live, w_o=w_o, eps=eps, scale=scale,
+                                      key_offset=key_offset, need_dvalues=need_dvalues, need_dlive=need_dlive,
+                                      dvalues=dvalues, workspace=workspace)
     D = int(D)
     src = _Sources(rows, attnres_cache_row_bytes(D, bits))
     dev, N, S = src.device, src.N, len(src.addrs)
@@ -326,7 +355,7 @@ def attnres_cached_bwd(rows: Records, q: torch.Tensor, dy: torch.Tensor, saved: 
     need = _workspace_bytes(p, dev)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-    _call("attnres_cached_bwd", dev, stream, ctypes.byref(p), q.data_ptr(), _addr(w_o), dy.data_ptr(),
+    _call("attnres_cached_bwd", dev, ctypes.byref(p), q.data_ptr(), _addr(w_o), dy.data_ptr(),
           saved["alpha"].data_ptr(), saved["rstd"].data_ptr(), saved["logit"].data_ptr(), _addr(saved.get("o_rstd")),
           dptrs, dld, _addr(d_live), D, dq.data_ptr(), dq32.data_ptr(), _addr(dw), _addr(dw32), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
@@ -348,7 +377,9 @@ def attnres_cached(rows: Records, query: torch.Tensor, D: int, *, bits: int = 8,
     The records are kept for the backward: until it has run no source read may
     be written again.  Autograd notices a write into a source's own tensor;
     sources that share one tensor (packed) count as written together, so give
-    each a tensor of its own where later ones are written before the backward."""
+    each a tensor of its own where later ones are written before the backward.
+    To capture the gradient in a CUDA graph use torch.autograd.grad, with no
+    eager graph of the same leaves alive."""
     from .custom_ops import attnres_cached_op
     return attnres_cached_op(rows, query, D, bits=bits, values=values, live=live, eps=eps, scale=scale,
                              out_norm_weight=out_norm_weight, key_offset=key_offset)

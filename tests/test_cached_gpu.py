@@ -358,6 +358,37 @@ def test_other_stream_and_graph():
             assert all(torch.equal(a[k], b[k]) for k in a if a[k] is not None)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_stream_argument(raw):
+    """A call on `stream` waits for nothing on the current one: the copies of
+    inputs that cannot be addressed in place, and what it allocates, are the
+    stream's too."""
+    S, N, D, bits = 3, 33, 136, 8
+    x, rows, _ = sources(S, N, D, bits, D, 0)
+    q, w, dy = rand((D,), 1, D ** -0.5), rand((D,), 2), rand((N, D), 3)
+    f = attnres_cached_fwd(rows, q, D, bits=bits, w_o=w)
+    g = attnres_cached_bwd(rows, q, dy, f, D, bits=bits, w_o=w)
+    odd = torch.empty(rows.numel() + 8, dtype=torch.uint8, device="cuda")[8:].view(rows.shape)
+    odd.copy_(rows)
+    xt, dyt, wide = x.transpose(1, 2).contiguous().transpose(1, 2), dy.t().contiguous().t(), rand((2 * D,), 5)
+    w2 = wide[::2].copy_(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                  # some 50 ms on the current stream
+    s = dict(bits=bits, stream=side.cuda_stream if raw else side)
+    r2 = attnres_cache_write(xt, **s)
+    v2 = attnres_cache_load(odd, D, **s)
+    f2 = attnres_cached_fwd(odd, q, D, w_o=w2, **s)
+    g2 = attnres_cached_bwd(odd, q, dyt, f2, D, w_o=w2, **s)
+    side.synchronize()
+    got = [t.cpu() for t in (r2, v2, f2["y"], f2["alpha"], g2["dvalues"], g2["dq_f32"], g2["dw_o_f32"])]
+    want = [rows, attnres_cache_load(rows, D, bits=bits), f["y"], f["alpha"], g["dvalues"], g["dq_f32"], g["dw_o_f32"]]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b.cpu())
+    with pytest.raises(ValueError):
+        attnres_cached_fwd([], q, D, **s)
+
+
 # ----------------------------------------------------------------- autograd
 @pytest.mark.parametrize("packed", [True, False])
 @pytest.mark.parametrize("bits", [8, 4])
