@@ -401,12 +401,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cached_bwd_kernel(const Cached
         }
         flip ^= 1;
         __syncwarp();
+        const long long to = (n * b.dsrc_ld + c0) * 2;  // of the thread's first channel in a source's gradient
+        const bool put = b.want_dsrc && valid;
+        const bool put0 = put && half[0] < a.D, put1 = put && half[1] < a.D;
         for (int u = 0; u < nseg; ++u) {
             next(2, u);
             const uint32_t base = st0 + stage * G::rows(seg);
             const int s0 = u * seg, cnt = min(seg, a.S - s0);
             auto store = [&](int s, const uint32_t (&o)[16]) {
-                if (b.want_dsrc && valid) store_halves(b.dsrc[s] + n * b.dsrc_ld, half, a.D, b.wide_src, o);
+                unsigned char* p = reinterpret_cast<unsigned char*>(b.dsrc[s]) + to;
+                if (b.wide_src) {
+                    store_half(p + 32 * sw, put0, o);
+                    store_half(p + 32 * (1 - sw), put1, o + 8);
+                } else if (put) {
+                    store_halves(reinterpret_cast<uint16_t*>(p) - c0, half, a.D, false, o);
+                }
             };
             // one row's gradient and its part of dq; RAGGED: some thread of the warp has channels outside the key
             auto grad = [&](auto ragged_c, int r, uint32_t (&h)[16], float row_scale) {

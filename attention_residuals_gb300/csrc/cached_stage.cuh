@@ -250,6 +250,14 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* p, int left, bool wide, 
     }
 }
 
+// 16 channels to a 32-byte aligned address.
+__device__ __forceinline__ void store_half(void* p, bool on, const uint32_t* w) {
+    if (on)
+        asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+}
+
 // The same from two runs of 16 channels, at channels half[0] and half[1] of a row.
 __device__ __forceinline__ void store_halves(uint16_t* row, const int (&half)[2], int D, bool wide, const uint32_t (&w)[16]) {
 #pragma unroll
