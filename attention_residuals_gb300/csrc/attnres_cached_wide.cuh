@@ -8,7 +8,10 @@
 // for nobody.  Segments of records come to the warp's own shared memory by
 // bulk copies, one a record; per segment
 //   1. dots with the query, halves by halves with FP32 sums (fma.rn.f32.f16),
-//      a block of rows at a time, so that the query is read once a block
+//      a block of rows at a time, so that the query is read once a block; the
+//      lanes' sums go to memory, where lane s adds row s's (five shuffles a
+//      block, each waiting for the one before, where that room would cost
+//      another segment)
 //   2. the running softmax, a lane a row
 //   3. mixture: codes decoded again, widened and added in FP32; a slot that
 //      has been read takes the next segment's record at once.
@@ -19,7 +22,10 @@
 // us in 8 (4.6 TB/s); 8 blocks and a live row, N=16384, R=1024, 8 bits: 144 us
 // (5.7 TB/s).  Twelve warps with spills took 383 us for 318, two warps of two
 // groups a token 320, a barrier of its own for a segment's first rows 300 for
-// 294.
+// 294, slots for a segment ahead (half as long segments) 321 for 299: the
+// steps between two segments' rows cost 0.8 us a token.  Dots by shuffles and
+// the softmax's sum over the warp once a segment: 299 for 294, S=64 N=8192
+// D=8192 in 8 bits 1196 for 1145.
 #pragma once
 
 #include <type_traits>
@@ -34,14 +40,16 @@ namespace {
 __device__ unsigned g_cached_wide_error;
 
 constexpr int kWideSmem = 227 * 1024;
+constexpr uint32_t kDotRow = 36 * 4;  // bytes of a row's 32 dots, a lane each (padded: lanes read four of their own row's at once)
 
 struct WidePlan {
     int seg;                  // records a segment, and slots a warp
+    int dots;                 // whether a warp has room for its lanes' dots of a segment
     uint32_t slot;            // bytes of a slot: the warp's part of a record
     uint32_t codes, scales;   // of a slot: bytes of codes, where the scales begin
     uint32_t stat;            // where the statistic is in a slot
     uint32_t q_at, w_at, rows_at, abort_at, warp_at, warp_bytes;  // shared memory: the CTA's, then the warps'
-    uint32_t red_at, coef_at, z_at, bar_at, live_at;                // in a warp's
+    uint32_t red_at, coef_at, z_at, bar_at, live_at, dots_at;       // in a warp's
     size_t smem;
 };
 
@@ -73,7 +81,7 @@ WidePlan wide_plan(int D, int S, bool live, bool norm, int bits, int nc, int w, 
     p.bar_at = take(16);  // of the rows and of the live row
     p.live_at = take(live ? nc * 2048 : 0);
     p.z_at = take(2 * SL * 4);
-    p.red_at = take(2 * 32 * 4);
+    p.red_at = take(w > 1 ? 2 * 32 * 4 : 0);
     p.coef_at = take(32 * 4);
     // lanes behind a row's last group read on from its end
     const uint32_t lanes = static_cast<uint32_t>(nc) * 32 * 4 * bits, over = lanes > p.slot ? lanes - p.slot : 0;
@@ -83,7 +91,11 @@ WidePlan wide_plan(int D, int S, bool live, bool norm, int bits, int nc, int w, 
     if (most < 1) most = 1;
     const int n = (S + most - 1) / most;
     p.seg = (S + n - 1) / n;
-    p.warp_bytes = off + ((p.seg * p.slot + 15) & ~15u);
+    // not at the price of another segment: S=32 N=16384 D=2048 and a live row,
+    // 4 bits, 201 us in four segments without the room, 214 in five with it
+    p.dots = p.seg * (p.slot + kDotRow) <= room;
+    p.dots_at = off + p.seg * p.slot;
+    p.warp_bytes = p.dots_at + p.dots * p.seg * kDotRow;
     p.smem = p.warp_at + static_cast<size_t>(warps) * p.warp_bytes + over;
     return p;
 }
@@ -103,7 +115,15 @@ __device__ __forceinline__ void query_halves(const CachedArgs& a, int c0, int sh
     }
 }
 
-template <int BITS, int NC, int W, int WARPS, bool NORM, bool LIVE>
+// Maximum over the warp, as integers of the same order.  A NaN counts as above
+// or below everything; the weights are NaN then either way.
+__device__ __forceinline__ float top_of(float z) {
+    const int b = __float_as_int(z), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+    return __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+}
+
+// DOTS: the warp has room for its lanes' dots of a segment.
+template <int BITS, int NC, int W, int WARPS, bool NORM, bool LIVE, bool DOTS>
 __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const CachedArgs a, const WidePlan pl) {
     constexpr int CH = BITS / 4;                  // 16-byte chunks of codes a group
     constexpr int K = BITS == 8 ? 2 : 4;          // rows of a block of dots
@@ -121,6 +141,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
     const uint32_t slots = smem_u32(own) + pl.coef_at + 128;
     float* zbuf = reinterpret_cast<float*>(own + pl.z_at);    // logits, then 1 / RMS (of the team's first warp)
     float* coef = reinterpret_cast<float*>(own + pl.coef_at);
+    float* dot_rows = reinterpret_cast<float*>(own + pl.dots_at);
     if (threadIdx.x == 0) *abort = 0;
     if (lane == 0) {
         for (int i = 0; i < 2; ++i) mbar_init(reinterpret_cast<uint64_t*>(own + pl.bar_at + 8 * i), 1);
@@ -252,7 +273,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
     }
     for (long long n = first; n < a.N; n += stride) {
         f2 acc[NC][16];
-        float mx, sum;
+        float mx, sum;  // of the softmax: the maximum, and the lane's part of the sum
         if constexpr (LIVE) {  // the live source first: it is the mixture, with weight 1
             float p0 = 0.0f, p1 = 0.0f;
             wait(1);
@@ -300,7 +321,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
             }
             const float rs = rsqrtf(p1 * inv_R + a.eps);
             mx = a.scale * rs * p0;
-            sum = mx == mx ? 1.0f : mx;  // a NaN stays one
+            sum = mx != mx ? mx : lane == 0 ? 1.0f : 0.0f;  // a NaN stays one
             if (w == 0 && lane == 0) zbuf[a.S] = mx, zbuf[SL + a.S] = rs;
         } else {
             mx = __uint_as_float(0xff800000u);
@@ -319,7 +340,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
             const long long nn = last ? n + stride : n;
             const int ns0 = last ? 0 : s0 + seg;
             const int ncnt = nn < a.N && !*abort ? min(seg, a.S - ns0) : 0;
-            float* dotbuf = coef;
+            float dot = 0.0f;  // of row `lane`
             if (any_keys) {
                 auto dots = [&](auto count, int r0) {
                     constexpr int M = decltype(count)::value;
@@ -356,19 +377,35 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
                             p[r] += key ? (d0 + d1) * f[r] : 0.0f;
                         }
                     }
-                    lanes_sum_to<32>(p, dotbuf + r0);
+                    if constexpr (DOTS) {
+#pragma unroll
+                        for (int r = 0; r < M; ++r) dot_rows[(r0 + r) * (kDotRow / 4) + lane] = p[r];
+                    } else {
+                        lanes_sum_to<32>(p, coef + r0);
+                    }
                 };
                 int r = 0;
 #pragma unroll 1
                 for (; r + K <= cnt; r += K) dots(std::integral_constant<int, K>{}, r);
                 if (K == 4 && r + 2 <= cnt) dots(std::integral_constant<int, 2>{}, r), r += 2;
                 if (r < cnt) dots(std::integral_constant<int, 1>{}, r);
-            } else {
-                dotbuf[lane] = 0.0f;
+                __syncwarp();
+                if (lane < cnt) {
+                    if constexpr (DOTS) {  // lane s adds row s's over the lanes: one wait for a segment, not five shuffles for each block
+                        f2 d0 = 0ull, d1 = 0ull;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(dot_rows + lane * (kDotRow / 4) + 4 * i);
+                            d0 = f2_add(d0, x.x), d1 = f2_add(d1, x.y);
+                        }
+                        dot = f2_sum(f2_add(d0, d1));
+                    } else {
+                        dot = coef[lane];
+                    }
+                }
             }
-            __syncwarp();
             // logits and weights of the segment: lane s has row s
-            const float dot = exchange(lane < cnt ? dotbuf[lane] : 0.0f) * back;
+            dot = exchange(dot) * back;
             float z = __uint_as_float(0xff800000u);
             if (lane < cnt) {
                 const uint32_t at = slots + lane * pl.slot + pl.stat;
@@ -378,11 +415,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
                 z = a.scale * rs * dot;
                 if (w == 0) zbuf[s0 + lane] = z, zbuf[SL + s0 + lane] = rs;
             }
-            const float mnew = fmaxf(mx, warp_max(z));
+            const float mnew = fmaxf(mx, top_of(z));
             const float e = lane < cnt ? __expf(z - mnew) : 0.0f, corr = __expf(mx - mnew);
             __syncwarp();
             coef[lane] = e;
-            sum = sum * corr + warp_sum(e);
+            sum = sum * corr + e;
             mx = mnew;
             if (LIVE || g > 0) {
 #pragma unroll
@@ -419,8 +456,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
             }
             if (r + lane < ncnt) fetch(nn, ns0 + r + lane, r + lane);
         }
-        const float inv = 1.0f / sum;
-        float post = inv;
+        float post;
         if constexpr (NORM) {
             if (any_cut && cut) {
 #pragma unroll
@@ -438,10 +474,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
                 for (int i = 0; i < 16; ++i) ss = f2_fma(acc[c][i], acc[c][i], ss);
                 if (has >> c & 1u) s1 += f2_sum(ss);
             }
-            s1 = exchange(warp_sum(s1));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {  // both at once
+                const float x = __shfl_xor_sync(0xffffffffu, s1, o), y = __shfl_xor_sync(0xffffffffu, sum, o);
+                s1 += x, sum += y;
+            }
+            const float inv = 1.0f / sum;
+            s1 = exchange(s1);
             const float o_rstd = rsqrtf(s1 * inv * inv * inv_D + a.eps);
             if (w == 0 && lane == 0) a.o_rstd[n] = o_rstd;
-            post *= o_rstd;
+            post = inv * o_rstd;
+        } else {
+            sum = warp_sum(sum);
+            post = 1.0f / sum;
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -467,7 +512,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
                 const float z = zbuf[s];
                 a.logit[n * SL + s] = z;
                 a.rstd[n * SL + s] = zbuf[SL + s];
-                a.alpha[n * SL + s] = __expf(z - mx) * inv;
+                a.alpha[n * SL + s] = __expf(z - mx) / sum;
             }
             __syncwarp();
         }
@@ -483,8 +528,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) cached_wide_kernel(const Cached
 template <int BITS, int NC, int W, int WARPS>
 cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
     const WidePlan p = wide_plan(a.D, a.S, a.live != nullptr, a.w_o != nullptr, BITS, NC, W, WARPS);
-    auto run = [&](auto norm, auto live) {
-        constexpr auto kern = cached_wide_kernel<BITS, NC, W, WARPS, decltype(norm)::value, decltype(live)::value>;
+    auto with = [&](auto norm, auto live, auto dots) {
+        constexpr auto kern =
+            cached_wide_kernel<BITS, NC, W, WARPS, decltype(norm)::value, decltype(live)::value, decltype(dots)::value>;
         int fit = 0;
         const cudaError_t err = kernel_fit<kern>(32 * WARPS, p.smem, &fit);
         if (err != cudaSuccess) return err;
@@ -494,6 +540,7 @@ cudaError_t launch_t(const CachedArgs& a, int sm_count, cudaStream_t stream) {
     };
     using Yes = std::true_type;
     using No = std::false_type;
+    auto run = [&](auto norm, auto live) { return p.dots ? with(norm, live, Yes{}) : with(norm, live, No{}); };
     return a.w_o ? (a.live ? run(Yes{}, Yes{}) : run(Yes{}, No{})) : (a.live ? run(No{}, Yes{}) : run(No{}, No{}));
 }
 
