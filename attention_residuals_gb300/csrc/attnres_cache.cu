@@ -11,8 +11,8 @@
 //
 // A lane takes 8 channels a load (16 bytes), so the group's maximum is two
 // shuffles.  What bounds the write: instructions and HBM together.  81920 rows
-// of D=4096 under counters: 171 us in 8 bits (5.9 TB/s, 0.68 of the issue
-// slots), 156 us in 4 (5.4 TB/s, 0.74).
+// of D=4096 under counters: 170 us in 8 bits (6.0 TB/s, 0.67 of the issue
+// slots), 156 us in 4 (5.4 TB/s, 0.73).
 //
 // Load: v = code * 2^k, exact in bf16; 16 channels a lane.  HBM bounds it: nine
 // sources of 8192 x 4096 from 4 bits in 119 us, 0.95 of the copy rate.

@@ -18,7 +18,7 @@
 //
 // What bounds it: latency at eight warps an SM (the sums and do fill the
 // registers), between bursts of gradient stores.  S=10 N=8192 D=4096 with the
-// norm: 259 us in 8 bits, 254 us in 4 (1.09 and 0.92 GB: 4.2 and 3.6 TB/s).
+// norm: 255 us in 8 bits, 249 us in 4 (1.09 and 0.92 GB: 4.3 and 3.7 TB/s).
 // Twelve warps, one buffer refilled row by row and dw_o in shared memory: 297
 // us for 259; without the norm at 168 registers in 4 bits, step 542 us for 467.
 #include <type_traits>

@@ -18,9 +18,9 @@
 // What bounds it: instruction issue.  Decoding costs half an instruction a
 // value and pass, the dot one, widening one, the packed FMA a half; at eight
 // warps an SM (the mixture fills the registers) half of the slots issue.
-// S=10 N=32768 D=4096 with the output norm: 294 us in 4 bits (3.4 TB/s), 359
-// us in 8 (4.6 TB/s); 8 blocks and a live row, N=16384, R=1024, 8 bits: 144 us
-// (5.7 TB/s).  Twelve warps with spills took 383 us for 318, two warps of two
+// S=10 N=32768 D=4096 with the output norm: 294 us in 4 bits (3.4 TB/s), 360
+// us in 8 (4.6 TB/s); 8 blocks and a live row, N=16384, R=1024, 8 bits: 140 us
+// (5.9 TB/s).  Twelve warps with spills took 383 us for 318, two warps of two
 // groups a token 320, a barrier of its own for a segment's first rows 300 for
 // 294, slots for a segment ahead (half as long segments) 321 for 299: the
 // steps between two segments' rows cost 0.8 us a token.  Dots by shuffles and
